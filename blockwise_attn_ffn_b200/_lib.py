@@ -16,8 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbpt.so")
 
 BPT_OK, BPT_ERR_INVALID_ARG, BPT_ERR_UNSUPPORTED, BPT_ERR_WORKSPACE, BPT_ERR_CUDA, \
-    BPT_ERR_TIMEOUT, BPT_ERR_RANGE = range(7)
-BPT_F32, BPT_BF16 = 0, 1
+    BPT_ERR_TIMEOUT, BPT_ERR_RANGE, BPT_ERR_INDEX = range(8)
+BPT_F32, BPT_BF16, BPT_F16 = 0, 1, 2
 KINDS = ["ln1", "qkv", "attn", "wo", "ln2", "w1", "w2", "cvt", "tail"]
 BPT_WAVE_BLOCKS = 256
 BPT_TAIL_MAX_PAIRS = 74
@@ -36,6 +36,8 @@ EXPORTED = [
     "bpt_layer_shard_workspace_size", "bpt_layer_shard_project", "bpt_layer_shard_forward",
     "bpt_layer_forward_train_keep_o", "bpt_layer_backward_keep_o",
     "bpt_layer_tail_plan",
+    "bpt_cache_workspace_size", "bpt_cache_append", "bpt_cache_evict",
+    "bpt_attn_decode_workspace_size", "bpt_attn_decode",
 ]
 
 
@@ -44,6 +46,16 @@ class Options(ctypes.Structure):
     _fields_ = [("schedule", ctypes.c_int32), ("attn_block", ctypes.c_int32),
                 ("max_wave", ctypes.c_int64), ("fault", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    """``bpt_cache`` (include/bpt.h): a paged key-value cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("d_k", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def make_options(schedule=None, attn_block=0, max_wave=0, fault=0, reserved=0) -> Options:
@@ -150,6 +162,17 @@ def load() -> ctypes.CDLL:
     lib.bpt_layer_tail_plan.restype = i32
     lib.bpt_layer_forward_static.argtypes = [vp] * 11 + [i64] * 5 + [i32, i32, vp, vp]
     lib.bpt_layer_forward_static.restype = i32
+    sz = ctypes.c_size_t
+    pc, pz, pi = ctypes.POINTER(Cache), ctypes.POINTER(sz), ctypes.POINTER(i64)
+    lib.bpt_cache_workspace_size.argtypes = [pc, pz]
+    lib.bpt_cache_append.argtypes = [pc, vp, vp, i64, pi] + [vp] * 6 + [sz, vp]
+    lib.bpt_cache_evict.argtypes = [pc, i64, i64, i64] + [vp] * 7 + [sz, vp]
+    lib.bpt_attn_decode_workspace_size.argtypes = [pc, i64, i32, pz]
+    lib.bpt_attn_decode.argtypes = [pc, vp, i64, i64, i64, i64, i64, vp, vp, vp, i64, i64, vp, sz,
+                                    vp]
+    for fn in (lib.bpt_cache_workspace_size, lib.bpt_cache_append, lib.bpt_cache_evict,
+               lib.bpt_attn_decode_workspace_size, lib.bpt_attn_decode):
+        fn.restype = i32
     _lib = lib
     return lib
 
@@ -366,3 +389,41 @@ def bpt_layer_tail_plan(B, N, d, h, d_ff, causal, resident_pairs, rows=None):
     n = min(pairs.value, rows) if st == BPT_OK else 0
     plan = [tuple(buf[5 * q:5 * q + 5]) for q in range(n)]
     return st, pairs.value, shared.value, plan
+
+
+# ------------------------------------------------- paged key-value cache --
+def bpt_cache_workspace_size(cache: Cache) -> Tuple[int, int]:
+    """Returns (status, bytes)."""
+    out = ctypes.c_size_t(0)
+    st = load().bpt_cache_workspace_size(ctypes.byref(cache), ctypes.byref(out))
+    return st, out.value
+
+
+def bpt_cache_append(cache, k_new, v_new, tokens, strides, counts, new_lens, acc, pos, seen,
+                     workspace, workspace_bytes, stream) -> int:
+    """Pointer-level call; strides is a (c_int64 * 6) array; returns the status."""
+    return load().bpt_cache_append(cache, k_new, v_new, tokens, strides, counts, new_lens, acc,
+                                   pos, seen, workspace, workspace_bytes, stream)
+
+
+def bpt_cache_evict(cache, budget, recent, sinks, acc, pos, seen, acc_out, pos_out, new_lens,
+                    workspace, workspace_bytes, stream) -> int:
+    """Pointer-level call; returns the status."""
+    return load().bpt_cache_evict(cache, budget, recent, sinks, acc, pos, seen, acc_out, pos_out,
+                                  new_lens, workspace, workspace_bytes, stream)
+
+
+def bpt_attn_decode_workspace_size(cache: Cache, heads, with_acc) -> Tuple[int, int]:
+    """Returns (status, bytes)."""
+    out = ctypes.c_size_t(0)
+    st = load().bpt_attn_decode_workspace_size(ctypes.byref(cache), heads, int(bool(with_acc)),
+                                               ctypes.byref(out))
+    return st, out.value
+
+
+def bpt_attn_decode(cache, q, heads, q_stride_b, q_stride_h, window, sinks, acc, acc_out, out,
+                    out_stride_b, out_stride_h, workspace, workspace_bytes, stream) -> int:
+    """Pointer-level call (acc, acc_out may be None); returns the status."""
+    return load().bpt_attn_decode(cache, q, heads, q_stride_b, q_stride_h, window, sinks, acc,
+                                  acc_out, out, out_stride_b, out_stride_h, workspace,
+                                  workspace_bytes, stream)

@@ -2,10 +2,11 @@
 
     python -m blockwise_attn_ffn_b200.build
 
-The library is one translation unit (csrc/bpt_api.cu including the kernel
-headers) linked against the static CUDA runtime; the driver API entry point it
-needs (tensor-map encoding) is resolved at run time, so no libcuda stub is
-linked.
+The library is two translation units (csrc/bpt_api.cu, the layer calls, and
+csrc/ops_api.cu, the attention operators and the key-value cache, each
+including its kernel headers), compiled side by side and linked against the
+static CUDA runtime; the driver API entry point they need (tensor-map
+encoding) is resolved at run time, so no libcuda stub is linked.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,9 +25,10 @@ LIB = os.path.join(HERE, "libbpt.so")
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
+UNITS = ["bpt_api.cu", "ops_api.cu"]
 
 
 def sources():
@@ -48,19 +51,31 @@ def nvcc() -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile csrc/bpt_api.cu into libbpt.so (skipped when up to date)."""
+    """Compile the units of csrc/ into libbpt.so (skipped when up to date)."""
     if not force and up_to_date():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I" + INCLUDE, "-I" + CSRC,
-           os.path.join(CSRC, "bpt_api.cu"), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    if verbose and (r.stdout or r.stderr):
-        print(r.stdout + r.stderr)
+    with tempfile.TemporaryDirectory() as obj_dir:
+        objs, jobs = [], []
+        for unit in UNITS:
+            objs.append(os.path.join(obj_dir, unit + ".o"))
+            cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I" + INCLUDE, "-I" + CSRC, "-c",
+                   os.path.join(CSRC, unit), "-o", objs[-1]]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            jobs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                         text=True))
+        outs = [j.communicate()[0] for j in jobs]
+        for job, out in zip(jobs, outs):
+            if job.returncode != 0:
+                raise RuntimeError("nvcc failed:\n" + out)
+            if verbose and out:
+                print(out)
+        r = subprocess.run([nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a",
+                            "-Xcompiler", "-fPIC", *objs, "-o", tmp], capture_output=True,
+                           text=True)
+        if r.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1938,6 +1938,7 @@ const char* bpt_status_string(bpt_status status) {
     case BPT_ERR_CUDA: return "BPT_ERR_CUDA: a CUDA call failed";
     case BPT_ERR_TIMEOUT: return "BPT_ERR_TIMEOUT: a kernel gave up waiting on a barrier";
     case BPT_ERR_RANGE: return "BPT_ERR_RANGE: a tensor-core operand exceeded the fp16 range";
+    case BPT_ERR_INDEX: return "BPT_ERR_INDEX: a length or page number outside the cache";
   }
   return "BPT_UNKNOWN_STATUS";
 }

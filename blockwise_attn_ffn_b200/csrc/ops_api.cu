@@ -1,0 +1,423 @@
+// Host side of the attention operators that stand beside the layer calls: the
+// paged key-value cache (append, one-token attention, eviction) and attention
+// with a sliding window (forward, backward).  Argument checks, workspace
+// layouts and launches; nothing is allocated and nothing synchronises.
+//
+// Workspaces: the first kOpsHeader bytes hold the error word, zeroed by the
+// caller once (bpt_read_device_error clears it after reading a fault), so a
+// call launches nothing but its own kernels.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <initializer_list>
+#include <mutex>
+
+#include "bpt.h"
+
+// The shared device helpers define functions in namespace bpt; in this unit
+// the namespace gets its own name, so that both units link into one library.
+#define bpt bpt_ops
+#include "attn_decode.cuh"
+#include "cache.cuh"
+#include "common.cuh"
+
+namespace {
+
+constexpr size_t kOpsHeader = 256;
+static_assert(bpt::kErrIndex == BPT_ERR_INDEX, "status code");
+
+size_t align_to(size_t v, size_t a) { return (v + a - 1) / a * a; }
+bool unaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+struct Range {
+  uintptr_t a, b;
+  Range(const void* p, size_t n)
+      : a(reinterpret_cast<uintptr_t>(p)), b(reinterpret_cast<uintptr_t>(p) + (p ? n : 0)) {}
+  bool meets(const Range& o) const { return a < o.b && o.a < b; }
+};
+bool any_meets(const Range& r, std::initializer_list<Range> others) {
+  for (const Range& o : others)
+    if (r.meets(o)) return true;
+  return false;
+}
+
+// Extent in bytes of a strided 16-bit array (strides in elements, >= 0).
+size_t extent(std::initializer_list<std::pair<int64_t, int64_t>> dims, int64_t last) {
+  int64_t e = last;
+  for (const auto& d : dims) e += (d.first - 1) * d.second;
+  return size_t(e) * 2;
+}
+
+// Streaming multiprocessors of the current device (an sm_100 GPU).
+struct OpsDevice {
+  bool init = false, ok = false;
+  int sms = 0;
+};
+std::mutex g_ops_mu;
+OpsDevice g_ops_dev[64];
+
+template <typename K>
+bool smem_fails(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+         cudaSuccess;
+}
+
+bpt_status ops_device(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return BPT_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_ops_mu);
+  OpsDevice& d = g_ops_dev[dev];
+  if (!d.init) {
+    int major = 0, minor = 0, n = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return BPT_ERR_CUDA;
+    d.ok = major == 10 && minor == 0;
+    d.sms = n;
+    using bf = __nv_bfloat16;
+    if (d.ok &&
+        (smem_fails(bpt::attn_decode_split_kernel<bf, 64>, bpt::DecodeCfg<64>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<bf, 128>, bpt::DecodeCfg<128>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<__half, 64>, bpt::DecodeCfg<64>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<__half, 128>, bpt::DecodeCfg<128>::SMEM)))
+      return BPT_ERR_CUDA;
+    d.init = true;
+  }
+  if (!d.ok) return BPT_ERR_UNSUPPORTED;
+  *sms = d.sms;
+  return BPT_OK;
+}
+
+// ------------------------------------------------------------------- cache --
+bpt_status check_cache(const bpt_cache* c) {
+  if (c == nullptr) return BPT_ERR_INVALID_ARG;
+  if (c->reserved != 0) return BPT_ERR_INVALID_ARG;
+  if (c->dtype != BPT_BF16 && c->dtype != BPT_F16) return BPT_ERR_INVALID_ARG;
+  if (c->batch < 0 || c->pages <= 0 || c->kv_heads <= 0 || c->page_size <= 0 || c->max_pages <= 0)
+    return BPT_ERR_INVALID_ARG;
+  if (c->d_k != 64 && c->d_k != 128) return BPT_ERR_UNSUPPORTED;
+  if (c->batch > 65535 || c->kv_heads > 65535) return BPT_ERR_UNSUPPORTED;
+  const int64_t lim = int64_t(1) << 31;
+  // rows and slots are 32-bit; byte offsets 64-bit
+  if (c->pages >= lim || c->page_size >= lim || c->max_pages >= lim) return BPT_ERR_UNSUPPORTED;
+  if (c->max_pages * c->page_size >= lim || c->pages * c->page_size >= lim ||
+      c->pages * c->page_size * c->kv_heads >= lim)
+    return BPT_ERR_UNSUPPORTED;
+  return BPT_OK;
+}
+bpt_status check_cache_pointers(const bpt_cache* c) {
+  for (const void* p : {c->k, c->v})
+    if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
+  for (const int32_t* p : {c->page_table, c->lens})
+    if (p == nullptr || unaligned(p, 4)) return BPT_ERR_INVALID_ARG;
+  const size_t n = size_t(c->pages) * size_t(c->kv_heads * c->page_size) * size_t(c->d_k) * 2;
+  if (Range(c->k, n).meets(Range(c->v, n))) return BPT_ERR_INVALID_ARG;
+  return BPT_OK;
+}
+size_t cache_bytes(const bpt_cache* c) {
+  return size_t(c->pages) * size_t(c->kv_heads * c->page_size) * size_t(c->d_k) * 2;
+}
+size_t slots_bytes(const bpt_cache* c) {  // [batch][kv_heads][max_pages * page_size] words
+  return size_t(c->batch) * size_t(c->kv_heads) * size_t(c->max_pages * c->page_size) * 4;
+}
+bpt::CacheView view_of(const bpt_cache* c, void* ws) {
+  bpt::CacheView v{};
+  v.k = static_cast<uint4*>(c->k);
+  v.v = static_cast<uint4*>(c->v);
+  v.table = c->page_table;
+  v.lens = c->lens;
+  v.pages = uint32_t(c->pages);
+  v.hkv = uint32_t(c->kv_heads);
+  v.ps = uint32_t(c->page_size);
+  v.max_pages = uint32_t(c->max_pages);
+  v.cap = uint32_t(c->max_pages * c->page_size);
+  v.err = static_cast<uint32_t*>(ws);
+  return v;
+}
+uint32_t clamp_u31(int64_t v) { return uint32_t(std::min<int64_t>(v, 0x7FFFFFFF)); }
+
+// Workspace of the cache's own operators: header, eviction lists and counts.
+struct CacheLayout {
+  size_t off_lists, off_count, total;
+};
+CacheLayout cache_layout(const bpt_cache* c) {
+  CacheLayout l{};
+  l.off_lists = kOpsHeader;
+  l.off_count = align_to(l.off_lists + slots_bytes(c), 256);
+  l.total = align_to(l.off_count + size_t(c->batch * c->kv_heads) * 4, 256);
+  return l;
+}
+
+struct DecodeLayout {
+  size_t off_o, off_ml, off_seg, off_scores, total;
+  int64_t chunks;
+};
+bpt_status decode_layout(const bpt_cache* c, int64_t heads, int with_acc, DecodeLayout* l) {
+  if (heads <= 0 || heads % c->kv_heads != 0) return BPT_ERR_INVALID_ARG;
+  const int64_t g = heads / c->kv_heads;
+  if (g > 256) return BPT_ERR_UNSUPPORTED;
+  l->chunks = (g + bpt::kDecodeRows - 1) / bpt::kDecodeRows;
+  const int64_t tiles = (c->max_pages * c->page_size + bpt::kDecodeTile - 1) / bpt::kDecodeTile;
+  const int64_t pairs = c->batch * c->kv_heads * l->chunks;
+  if (pairs >= (int64_t(1) << 31) || (pairs > 0 && tiles >= (int64_t(1) << 31) / pairs) ||
+      c->batch * c->kv_heads >= (int64_t(1) << 31))
+    return BPT_ERR_UNSUPPORTED;
+  const size_t parts = size_t(2 * bpt::kDecodeCtasPerSm * bpt::kDecodeMaxSms) * 16;
+  l->off_o = kOpsHeader;
+  l->off_ml = align_to(l->off_o + parts * size_t(c->d_k) * 4, 256);
+  l->off_seg = align_to(l->off_ml + parts * 8, 256);
+  l->off_scores = align_to(l->off_seg + size_t(pairs) * 16 * 8, 256);
+  l->total = l->off_scores;
+  if (with_acc)
+    l->total = align_to(l->off_scores + size_t(c->batch * heads) *
+                                            size_t(c->max_pages * c->page_size) * 4, 256);
+  return BPT_OK;
+}
+
+template <typename T, int D>
+cudaError_t launch_decode(const bpt::DecodeParams& p, unsigned slot_blocks, cudaStream_t s) {
+  bpt::attn_decode_split_kernel<T, D>
+      <<<p.ctas, bpt::kDecodeThreads, bpt::DecodeCfg<D>::SMEM, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  bpt::attn_decode_join_kernel<T, D>
+      <<<dim3(p.B * p.c.hkv, 1 + slot_blocks), bpt::kJoinThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+extern "C" {
+
+bpt_status bpt_cache_workspace_size(const bpt_cache* cache, size_t* bytes) {
+  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
+  const bpt_status st = check_cache(cache);
+  if (st != BPT_OK) return st;
+  *bytes = cache_layout(cache).total;
+  return BPT_OK;
+}
+
+bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const void* v_new,
+                            int64_t tokens, const int64_t* strides, const int32_t* counts,
+                            int32_t* new_lens, float* acc, int32_t* pos, const int32_t* seen,
+                            void* workspace, size_t workspace_bytes, bpt_stream_t stream) {
+  bpt_status st = check_cache(cache);
+  if (st != BPT_OK) return st;
+  if (tokens < 0) return BPT_ERR_INVALID_ARG;
+  if (cache->batch == 0) return BPT_OK;
+  st = check_cache_pointers(cache);
+  if (st != BPT_OK) return st;
+  const int64_t B = cache->batch, h = cache->kv_heads, dk = cache->d_k;
+  if (new_lens == nullptr || unaligned(new_lens, 4) || workspace == nullptr ||
+      unaligned(workspace, 256) || unaligned(counts, 4) || unaligned(acc, 4) ||
+      unaligned(pos, 4) || unaligned(seen, 4) || strides == nullptr)
+    return BPT_ERR_INVALID_ARG;
+  if (workspace_bytes < kOpsHeader) return BPT_ERR_WORKSPACE;
+  if (tokens > 0) {
+    for (const void* p : {k_new, v_new})
+      if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
+    for (int i = 0; i < 6; ++i)
+      if (strides[i] < 0 || strides[i] % 8 != 0) return BPT_ERR_INVALID_ARG;
+    if (tokens >= (int64_t(1) << 31) / (h * dk / 8)) return BPT_ERR_UNSUPPORTED;
+  }
+  const Range rk(cache->k, cache_bytes(cache)), rv(cache->v, cache_bytes(cache)),
+      rl(cache->lens, size_t(B) * 4), rn(new_lens, size_t(B) * 4),
+      rt(cache->page_table, size_t(B * cache->max_pages) * 4), ra(acc, slots_bytes(cache)),
+      rp(pos, slots_bytes(cache)), rc(counts, size_t(B) * 4), rs(seen, size_t(B) * 4),
+      rw(workspace, kOpsHeader);
+  const size_t kb = tokens > 0 ? extent({{B, strides[0]}, {tokens, strides[1]}, {h, strides[2]}}, dk) : 0;
+  const size_t vb = tokens > 0 ? extent({{B, strides[3]}, {tokens, strides[4]}, {h, strides[5]}}, dk) : 0;
+  const Range ik(k_new, kb), iv(v_new, vb);
+  // every array that is written meets no other one
+  if (any_meets(rk, {ik, iv, rl, rn, rt, ra, rp, rc, rs, rw}) ||
+      any_meets(rv, {ik, iv, rl, rn, rt, ra, rp, rc, rs, rw}) ||
+      any_meets(rn, {ik, iv, rl, rt, ra, rp, rc, rs, rw}) ||
+      any_meets(ra, {ik, iv, rl, rt, rp, rc, rs, rw}) ||
+      any_meets(rp, {ik, iv, rl, rt, rc, rs, rw}) || any_meets(rw, {ik, iv, rl, rt, rc, rs}))
+    return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  bpt::AppendParams p{};
+  p.c = view_of(cache, workspace);
+  p.k = static_cast<const uint4*>(k_new);
+  p.v = static_cast<const uint4*>(v_new);
+  p.k_b = strides[0] / 8;
+  p.k_t = strides[1] / 8;
+  p.k_h = strides[2] / 8;
+  p.v_b = strides[3] / 8;
+  p.v_t = strides[4] / 8;
+  p.v_h = strides[5] / 8;
+  p.counts = counts;
+  p.new_lens = new_lens;
+  p.acc = acc;
+  p.pos = pos;
+  p.seen = seen;
+  p.T = uint32_t(tokens);
+  p.row16 = uint32_t(dk / 8);
+  const int64_t per_block = bpt::kAppendThreads * bpt::kAppendUnroll;
+  const int64_t blocks = std::max<int64_t>(1, (tokens * h * (dk / 8) + per_block - 1) / per_block);
+  bpt::cache_append_kernel<<<dim3(unsigned(blocks), unsigned(B)), bpt::kAppendThreads, 0,
+                             reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recent, int64_t sinks,
+                           const float* acc, const int32_t* pos, const int32_t* seen,
+                           float* acc_out, int32_t* pos_out, int32_t* new_lens, void* workspace,
+                           size_t workspace_bytes, bpt_stream_t stream) {
+  bpt_status st = check_cache(cache);
+  if (st != BPT_OK) return st;
+  if (budget <= 0 || recent < 0 || sinks < 0) return BPT_ERR_INVALID_ARG;
+  if (cache->batch == 0) return BPT_OK;
+  st = check_cache_pointers(cache);
+  if (st != BPT_OK) return st;
+  const int64_t B = cache->batch;
+  for (const void* p : {static_cast<const void*>(acc), static_cast<const void*>(pos),
+                        static_cast<const void*>(seen), static_cast<const void*>(acc_out),
+                        static_cast<const void*>(pos_out), static_cast<const void*>(new_lens)})
+    if (p == nullptr || unaligned(p, 4)) return BPT_ERR_INVALID_ARG;
+  if (workspace == nullptr || unaligned(workspace, 256)) return BPT_ERR_INVALID_ARG;
+  const CacheLayout l = cache_layout(cache);
+  if (workspace_bytes < l.total) return BPT_ERR_WORKSPACE;
+  const size_t sb = slots_bytes(cache);
+  const Range rk(cache->k, cache_bytes(cache)), rv(cache->v, cache_bytes(cache)),
+      rl(cache->lens, size_t(B) * 4), rn(new_lens, size_t(B) * 4),
+      rt(cache->page_table, size_t(B * cache->max_pages) * 4), ra(acc, sb), rp(pos, sb),
+      rao(acc_out, sb), rpo(pos_out, sb), rs(seen, size_t(B) * 4), rw(workspace, l.total);
+  // the state may be updated in place (acc_out == acc, pos_out == pos,
+  // new_lens == lens); nothing else that is written meets another array
+  if ((acc_out != acc && rao.meets(ra)) || (pos_out != pos && rpo.meets(rp)) ||
+      (new_lens != cache->lens && rn.meets(rl)) ||
+      any_meets(rao, {rp, rpo, rk, rv, rl, rn, rt, rs, rw}) ||
+      any_meets(rpo, {ra, rk, rv, rl, rn, rt, rs, rw}) ||
+      any_meets(rk, {ra, rp, rl, rn, rt, rs, rw}) || any_meets(rv, {ra, rp, rl, rn, rt, rs, rw}) ||
+      any_meets(rn, {ra, rp, rt, rs, rw}) || any_meets(rw, {ra, rp, rl, rt, rs}))
+    return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  bpt::EvictParams p{};
+  p.c = view_of(cache, workspace);
+  p.acc = acc;
+  p.pos = pos;
+  p.seen = seen;
+  p.acc_out = acc_out;
+  p.pos_out = pos_out;
+  p.new_lens = new_lens;
+  p.budget = clamp_u31(budget);
+  p.recent = clamp_u31(recent);
+  p.sinks = clamp_u31(sinks);
+  p.row16 = uint32_t(cache->d_k / 8);
+  p.lists = reinterpret_cast<int*>(ws + l.off_lists);
+  p.count = reinterpret_cast<int*>(ws + l.off_count);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned hkv = unsigned(cache->kv_heads);
+  bpt::cache_evict_select_kernel<<<dim3(hkv, unsigned(B)), bpt::kEvictThreads, 0, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return BPT_ERR_CUDA;
+  // at most min(budget, capacity / 2) rows of a pair move; enough blocks to
+  // fill the device, at least one step each
+  const int64_t moves = std::min<int64_t>(p.budget, int64_t(p.c.cap) / 2);
+  const int64_t steps = (moves + bpt::kMoveRows - 1) / bpt::kMoveRows;
+  const int64_t fill = std::max<int64_t>(1, int64_t(sms) * 32 / (B * int64_t(hkv)));
+  const unsigned gx = unsigned(std::max<int64_t>(1, std::min(steps, fill)));
+  bpt::cache_evict_move_kernel<<<dim3(gx, hkv, unsigned(B)), bpt::kMoveThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status bpt_attn_decode_workspace_size(const bpt_cache* cache, int64_t heads, int with_acc,
+                                          size_t* bytes) {
+  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
+  bpt_status st = check_cache(cache);
+  if (st != BPT_OK) return st;
+  DecodeLayout l;
+  st = decode_layout(cache, heads, with_acc, &l);
+  if (st != BPT_OK) return st;
+  *bytes = l.total;
+  return BPT_OK;
+}
+
+bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
+                           int64_t q_stride_b, int64_t q_stride_h, int64_t window, int64_t sinks,
+                           const float* acc, float* acc_out, void* out, int64_t out_stride_b,
+                           int64_t out_stride_h, void* workspace, size_t workspace_bytes,
+                           bpt_stream_t stream) {
+  bpt_status st = check_cache(cache);
+  if (st != BPT_OK) return st;
+  if (window < 0 || sinks < 0 || (acc == nullptr) != (acc_out == nullptr))
+    return BPT_ERR_INVALID_ARG;
+  DecodeLayout l;
+  st = decode_layout(cache, heads, acc != nullptr, &l);
+  if (st != BPT_OK) return st;
+  if (cache->batch == 0) return BPT_OK;
+  st = check_cache_pointers(cache);
+  if (st != BPT_OK) return st;
+  const int64_t B = cache->batch, dk = cache->d_k;
+  for (const void* p : {q, static_cast<const void*>(out)})
+    if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
+  for (int64_t x : {q_stride_b, q_stride_h, out_stride_b, out_stride_h})
+    if (x < 0 || x % 8 != 0) return BPT_ERR_INVALID_ARG;
+  // output rows must not meet one another
+  if ((heads > 1 && out_stride_h < dk) || (B > 1 && out_stride_b < dk) ||
+      (B > 1 && heads > 1 && out_stride_b < (heads - 1) * out_stride_h + dk &&
+       out_stride_h < (B - 1) * out_stride_b + dk))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace == nullptr || unaligned(workspace, 256) || unaligned(acc, 4) ||
+      unaligned(acc_out, 4))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace_bytes < l.total) return BPT_ERR_WORKSPACE;
+  const Range rk(cache->k, cache_bytes(cache)), rv(cache->v, cache_bytes(cache)),
+      rl(cache->lens, size_t(B) * 4), rt(cache->page_table, size_t(B * cache->max_pages) * 4),
+      ra(acc, acc ? slots_bytes(cache) : 0), rao(acc_out, acc ? slots_bytes(cache) : 0),
+      rq(q, extent({{B, q_stride_b}, {heads, q_stride_h}}, dk)),
+      ro(out, extent({{B, out_stride_b}, {heads, out_stride_h}}, dk)), rw(workspace, l.total);
+  // acc may be updated in place; nothing else that is written meets another array
+  if ((acc_out != acc && rao.meets(ra)) || any_meets(rao, {rk, rv, rl, rt, rq, ro, rw}) ||
+      any_meets(ro, {rk, rv, rl, rt, rq, ra, rw}) || any_meets(rw, {rk, rv, rl, rt, rq, ra}))
+    return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  bpt::DecodeParams p{};
+  p.c = view_of(cache, workspace);
+  p.q = q;
+  p.q_b = q_stride_b;
+  p.q_h = q_stride_h;
+  p.out = out;
+  p.o_b = out_stride_b;
+  p.o_h = out_stride_h;
+  p.B = uint32_t(B);
+  p.h = uint32_t(heads);
+  p.g = uint32_t(heads / cache->kv_heads);
+  p.chunks = uint32_t(l.chunks);
+  p.window = clamp_u31(window);
+  p.sinks = clamp_u31(sinks);
+  p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
+  p.part_o = reinterpret_cast<float*>(ws + l.off_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + l.off_ml);
+  p.seg_ml = reinterpret_cast<float2*>(ws + l.off_seg);
+  p.ctas = uint32_t(bpt::kDecodeCtasPerSm * std::min(sms, bpt::kDecodeMaxSms));
+  p.scores = acc != nullptr ? reinterpret_cast<float*>(ws + l.off_scores) : nullptr;
+  p.acc = acc;
+  p.acc_out = acc_out;
+  const unsigned slot_blocks =
+      acc != nullptr ? unsigned((p.c.cap + bpt::kJoinSlots - 1) / bpt::kJoinSlots) : 0u;
+  if (slot_blocks > 65000) return BPT_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cache->dtype == BPT_BF16)
+    e = dk == 128 ? launch_decode<__nv_bfloat16, 128>(p, slot_blocks, s)
+                  : launch_decode<__nv_bfloat16, 64>(p, slot_blocks, s);
+  else
+    e = dk == 128 ? launch_decode<__half, 128>(p, slot_blocks, s)
+                  : launch_decode<__half, 64>(p, slot_blocks, s);
+  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -65,13 +65,16 @@ typedef enum {
   BPT_ERR_WORKSPACE = 3,   /* workspace smaller than bpt_layer_workspace_size */
   BPT_ERR_CUDA = 4,        /* a CUDA runtime / driver call failed */
   BPT_ERR_TIMEOUT = 5,     /* a kernel gave up waiting (device error word) */
-  BPT_ERR_RANGE = 6        /* an fp16 tensor-core operand overflowed (device error word) */
+  BPT_ERR_RANGE = 6,       /* an fp16 tensor-core operand overflowed (device error word) */
+  BPT_ERR_INDEX = 7        /* a cache length or page number outside the cache (device error word) */
 } bpt_status;
 
 typedef enum {
   BPT_F32 = 0,  /* x, weights, params fp32; fp32 arithmetic on CUDA cores */
-  BPT_BF16 = 1  /* x, weights, params bf16; tensor cores with fp16 operands
+  BPT_BF16 = 1, /* x, weights, params bf16; tensor cores with fp16 operands
                    (see below), fp32 accumulation */
+  BPT_F16 = 2   /* the attention operators and caches only; the layer calls
+                   take BPT_F32 and BPT_BF16 */
 } bpt_dtype;
 
 /* Same object as cudaStream_t; 0 is the legacy default stream. */
@@ -589,6 +592,109 @@ bpt_status bpt_layer_forward_static(const void* x, const void* ln1, const void* 
                                     const void* W_2, const void* b_2, int64_t B, int64_t N,
                                     int64_t d, int64_t h, int64_t d_ff, int causal,
                                     bpt_dtype dtype, float* out, bpt_stream_t stream);
+
+/* ------------------------------------------------- paged key-value cache --
+ * The keys and values that a decoding program keeps, and the operators on
+ * them.  K and V are [pages, kv_heads, page_size, d_k] arrays of 16-bit
+ * elements (dtype BPT_BF16 or BPT_F16, d_k 64 or 128, contiguous).  Slot s of
+ * sequence b is row s % page_size of page page_table[b][s / page_size], for
+ * every head; lens[b] slots hold tokens, page_table [batch, max_pages] names
+ * the pages of max_pages * page_size slots.  Entries for pages past the
+ * sequence's last slot are not read.  A page that two sequences share may be
+ * read by both; writing to it (append, evict) through both is undefined.
+ *
+ * State beside the rows, one word per (sequence, kv head, slot), arrays
+ * [batch, kv_heads, max_pages * page_size]:
+ *   acc  fp32, the attention weight the slot has received so far
+ *   pos  int32, the position of the slot's token in its sequence
+ * Words of slots past the sequence's length are neither read nor written.
+ *
+ * Lengths and page numbers live on the device and are checked there: a
+ * length outside 0 .. max_pages * page_size is taken as the nearest of the
+ * two, a page outside the pool is skipped (its slots count as not visible,
+ * its rows are not written), and BPT_ERR_INDEX is recorded for
+ * bpt_read_device_error.
+ *
+ * Workspaces of these operators: 256-byte aligned, the FIRST 256 BYTES ZEROED
+ * BY THE CALLER ONCE before the first use (the error word lives there; it
+ * keeps the first fault until bpt_read_device_error returns and clears it).
+ * The rest needs no initialisation.  Calls that may overlap on the GPU
+ * (different streams, graphs launched side by side) need a workspace each.
+ * All calls may be captured into a CUDA graph.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* page_table; /* [batch, max_pages] */
+  const int32_t* lens;       /* [batch] */
+  int64_t batch, pages, kv_heads, page_size, d_k, max_pages;
+  int32_t dtype;             /* BPT_BF16 or BPT_F16 */
+  int32_t reserved;          /* 0 */
+} bpt_cache;
+
+/* Workspace bytes of bpt_cache_append and bpt_cache_evict (pointers of the
+ * cache are not looked at).  Append alone needs only the 256-byte header. */
+bpt_status bpt_cache_workspace_size(const bpt_cache* cache, size_t* bytes);
+
+/*
+ * bpt_cache_append -- write new tokens behind each sequence.
+ * k_new, v_new: [batch, tokens, kv_heads, d_k], 16-byte aligned, element
+ * strides in strides[6] = {k: batch, token, head; v: batch, token, head},
+ * multiples of 8, last dimension contiguous.  counts (nullable, [batch]):
+ * sequence b gets its first counts[b] <= tokens of them (NULL: all).  Token t
+ * goes to slot lens[b] + t; new_lens[b] = lens[b] + its count.  new_lens may
+ * not be the lens array (blocks of one launch read the old lengths while
+ * others finish): swap the two.  acc, pos (nullable): the new slots get
+ * acc = 0 and pos = seen[b] + t (seen NULL: the slot number).  Tokens past
+ * the table's capacity are dropped and BPT_ERR_INDEX is recorded.
+ * lens itself is not changed.  BPT_ERR_UNSUPPORTED: d_k other than 64 / 128,
+ * 2^31 or more rows in the pool or slots in a table.
+ */
+bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const void* v_new,
+                            int64_t tokens, const int64_t* strides, const int32_t* counts,
+                            int32_t* new_lens, float* acc, int32_t* pos, const int32_t* seen,
+                            void* workspace, size_t workspace_bytes, bpt_stream_t stream);
+
+/*
+ * bpt_cache_evict -- cut every (sequence, kv head) to at most `budget` slots.
+ * With n = lens[b] > budget, the kept slots are: first the protected ones
+ * (pos < sinks, the first tokens; pos >= seen[b] - recent, the latest), then
+ * those of the largest acc, budget in all; equal weights (and, if there are
+ * more protected slots than budget, protected ones) by the lowest slot; NaN
+ * weights last.  Kept slots past the budget, in ascending order, move into
+ * the freed slots before it, in ascending order: rows of K and V in place in
+ * the pages, their acc and pos into acc_out and pos_out.  For the other kept
+ * slots acc_out and pos_out get acc and pos; nothing past the new length is
+ * written.  n <= budget: acc and pos are copied, no row moves.
+ * new_lens[b] = min(n, budget).  acc_out may be acc, pos_out pos and new_lens
+ * lens (exactly); they may not overlap otherwise.
+ */
+bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recent, int64_t sinks,
+                           const float* acc, const int32_t* pos, const int32_t* seen,
+                           float* acc_out, int32_t* pos_out, int32_t* new_lens, void* workspace,
+                           size_t workspace_bytes, bpt_stream_t stream);
+
+/*
+ * bpt_attn_decode -- attention of one new token per sequence over its cache.
+ * q, out: [batch, heads, d_k] of the cache's type, element strides
+ * (multiples of 8) given; kv_heads divides heads, head t reads kv head
+ * t / (heads / kv_heads), at most 256 heads per kv head.  Slot j < lens[b] is
+ * visible if window == 0, j >= lens[b] - window or j < sinks:
+ *   out[b, t] = sum_j softmax_j(q . k_j / sqrt(d_k)) v_j
+ * (append the new token first, so that it sees itself).  A sequence without
+ * visible slots gets zeros.  acc, acc_out (both or neither): for every slot
+ * j < lens[b], acc_out = acc + the sum over the kv head's query heads of the
+ * softmax weights (slots that are not visible add 0); acc_out may be acc.
+ * Scores, softmax statistics and sums are fp32; results do not depend on
+ * timing (no atomics).
+ */
+bpt_status bpt_attn_decode_workspace_size(const bpt_cache* cache, int64_t heads, int with_acc,
+                                          size_t* bytes);
+bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
+                           int64_t q_stride_b, int64_t q_stride_h, int64_t window, int64_t sinks,
+                           const float* acc, float* acc_out, void* out, int64_t out_stride_b,
+                           int64_t out_stride_h, void* workspace, size_t workspace_bytes,
+                           bpt_stream_t stream);
 
 #ifdef __cplusplus
 }
