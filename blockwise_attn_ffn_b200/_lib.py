@@ -38,6 +38,7 @@ EXPORTED = [
     "bpt_layer_tail_plan",
     "bpt_cache_workspace_size", "bpt_cache_append", "bpt_cache_evict",
     "bpt_attn_decode_workspace_size", "bpt_attn_decode",
+    "bpt_attn_window_workspace_size", "bpt_attn_window_forward",
 ]
 
 
@@ -56,6 +57,20 @@ class Cache(ctypes.Structure):
                 ("kv_heads", ctypes.c_int64), ("page_size", ctypes.c_int64),
                 ("d_k", ctypes.c_int64), ("max_pages", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Window(ctypes.Structure):
+    """``bpt_window`` (include/bpt.h): sizes of an attention with a window."""
+    _fields_ = [("batch", ctypes.c_int64), ("n_q", ctypes.c_int64), ("n_kv", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("d_k", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    """``bpt_rows`` (include/bpt.h): strided rows of 16-bit elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
 
 
 def make_options(schedule=None, attn_block=0, max_wave=0, fault=0, reserved=0) -> Options:
@@ -170,8 +185,12 @@ def load() -> ctypes.CDLL:
     lib.bpt_attn_decode_workspace_size.argtypes = [pc, i64, i32, pz]
     lib.bpt_attn_decode.argtypes = [pc, vp, i64, i64, i64, i64, i64, vp, vp, vp, i64, i64, vp, sz,
                                     vp]
+    pw, pr = ctypes.POINTER(Window), ctypes.POINTER(Rows)
+    lib.bpt_attn_window_workspace_size.argtypes = [pw, pz]
+    lib.bpt_attn_window_forward.argtypes = [pw, pr, pr, pr, vp, pr, vp, vp, sz, vp]
     for fn in (lib.bpt_cache_workspace_size, lib.bpt_cache_append, lib.bpt_cache_evict,
-               lib.bpt_attn_decode_workspace_size, lib.bpt_attn_decode):
+               lib.bpt_attn_decode_workspace_size, lib.bpt_attn_decode,
+               lib.bpt_attn_window_workspace_size, lib.bpt_attn_window_forward):
         fn.restype = i32
     _lib = lib
     return lib
@@ -427,3 +446,18 @@ def bpt_attn_decode(cache, q, heads, q_stride_b, q_stride_h, window, sinks, acc,
     return load().bpt_attn_decode(cache, q, heads, q_stride_b, q_stride_h, window, sinks, acc,
                                   acc_out, out, out_stride_b, out_stride_h, workspace,
                                   workspace_bytes, stream)
+
+
+# ------------------------------------- attention with a sliding window --
+def bpt_attn_window_workspace_size(window: Window) -> Tuple[int, int]:
+    """Returns (status, bytes)."""
+    out = ctypes.c_size_t(0)
+    st = load().bpt_attn_window_workspace_size(ctypes.byref(window), ctypes.byref(out))
+    return st, out.value
+
+
+def bpt_attn_window_forward(window, q, k, v, lens, out, stats, workspace, workspace_bytes,
+                            stream) -> int:
+    """Pointer-level call (lens, stats may be None); returns the status."""
+    return load().bpt_attn_window_forward(window, q, k, v, lens, out, stats, workspace,
+                                          workspace_bytes, stream)

@@ -1,0 +1,590 @@
+// Attention with a sliding window and sinks on the tcgen05 tensor cores,
+// forward.
+//
+// Query i stands at position p = nkv - nq + i and sees key j if
+// j <= p < len and (p - j < window or j < sinks); heads h / h_kv share a
+// key/value head.  Per row the online softmax keeps a reference maximum m, the
+// sum l and the accumulator o:
+//   S = Q K^T, P = exp2((S - m) log2(e)/sqrt(d_k)), l = alpha l + rowsum(P),
+//   O = alpha O + P V; at the end o = O / l.
+//
+// Only key tiles that a row of the CTA sees are loaded: work is
+// O(nq (window + sinks)), and the tensor cores bound it (4 d_k flops per
+// visible pair against 2 bytes of K and V per key and 256 rows).
+//
+// A CTA owns one kv head and two 128-row query tiles A and B that are
+// neighbours in the order (query block, head of the group): with shared heads
+// both tiles have the same keys, without they are consecutive blocks.  Each
+// K/V tile is loaded once for both.  Its keys are two lists of 128-key tiles:
+// sink tiles (keys 0 .. min(sinks, lo) - 1 from key 0) and window tiles, which
+// END at the last key any row sees, so that keys past a sequence's length are
+// not touched, and start where they must (TMA rows need no alignment; keys
+// before 0 read as zeros and are masked).  A tile that one of A and B does not
+// see is skipped for it.
+//
+// The schedule is that of the dense kernel: warp 0 loads (TMA), warp 1 issues
+// PV_A(j), S_A(j+1), PV_B(j), S_B(j+1) ..., four warps per tile run the
+// softmax; P stays in tensor memory over S.  The reference moves only when a
+// row's maximum grows by more than 2^8 (exp2 units).  P is rounded to the
+// operands' type for the product with V (half a step per weight, of both
+// signs); scores, statistics and O are fp32; l sums the unrounded weights.
+//
+// A masked key has weight 0, but 0 x V_j is NaN if V_j holds NaN or infinity.
+// Rows whose result is not finite are therefore done again, key by key over
+// what they see (window_row_slow): exact, and free for finite values.
+#pragma once
+
+#include <type_traits>
+
+#include "cache.cuh"
+#include "common.cuh"
+
+namespace bpt {
+
+enum : uint32_t { kSiteWindowLens = 19 };
+
+struct WindowParams {
+  int nq, nkv, h, hkv, g;   // g = h / hkv
+  int units, npairs;        // per (sequence, kv head): query blocks x g; CTAs
+  int window, sinks;
+  const int* lens;          // nullable [B]
+  const void* q;            // strided rows, elements (the slow path's loads)
+  const void* k;
+  const void* v;
+  long long q_b, q_n, q_h, k_b, k_n, k_h, v_b, v_n, v_h;
+  void* o;
+  long long o_b, o_n, o_h;
+  float scale_log2;         // log2(e) / sqrt(d_k)
+  float2* stats;            // nullable [B][h][nq]: (m, l), (-inf, 0) for rows past the length
+  uint32_t* err;
+};
+
+template <int D>
+struct WindowCfg {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int NSLOT = D == 128 ? 5 : 10;
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_RING + NSLOT * TILE;
+  static constexpr int SMEM = OFF_BAR + 512 + 1024;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t TM_S_B = 128, TM_O_A = 256, TM_O_B = 256 + D;
+  static constexpr int THREADS = 384;
+  // P hand-overs per 128-key tile to the issuing warp (measured on the dense
+  // kernel: 64 keys at a time at d_k = 128, 32 at d_k = 64)
+  static constexpr int HAND = D == 128 ? 2 : 4;
+};
+
+// Instruction descriptor of kind::f16 for this type (A, B: 0 fp16, 1 bf16).
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc16(int M, int N, bool a_mn, bool b_mn) {
+  const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return idesc_f16_f32(M, N, a_mn, b_mn) | (f << 7) | (f << 10);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value)
+    return pack_f16x2(lo, hi);
+  else
+    return pack_bf16x2(lo, hi);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack16(uint32_t v) {
+  if constexpr (std::is_same<T, __half>::value)
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  else
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+
+// Bits 0 .. n-1 of a word.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+// Bits a .. b-1 of the word that holds bits 32 w ...
+__device__ __forceinline__ uint32_t bits_range(int a, int b, int w) {
+  return bits_below(b - 32 * w) & ~bits_below(a - 32 * w);
+}
+
+__device__ __forceinline__ int window_len(const WindowParams& p, int b) {
+  if (p.lens == nullptr) return p.nkv;
+  const int n = __ldg(p.lens + b);
+  if (n < 0 || n > p.nkv) {
+    if (threadIdx.x == 0) record_error(p.err, kErrIndex, kSiteWindowLens);
+    return n < 0 ? 0 : p.nkv;
+  }
+  return n;
+}
+
+// Keys of a query tile: rows at positions p0 .. p0 + 127, the last valid one
+// before `end`.
+struct WindowTile {
+  int p0, lo, hi;  // visible window keys lo .. hi - 1; hi <= p0: no valid row
+  __device__ __forceinline__ bool any() const { return hi > p0; }
+};
+__device__ __forceinline__ WindowTile window_tile(const WindowParams& p, int qb, int len) {
+  WindowTile t;
+  const int off = p.nkv - p.nq;
+  t.p0 = off + qb * 128;
+  t.hi = min(off + min(p.nq, qb * 128 + 128), len);
+  t.lo = max(0, t.p0 - p.window + 1);
+  return t;
+}
+
+// The visible bits of keys kb + 32 w .. of a window tile for the row at p:
+// keys lo .. p that are within the window or sinks.
+__device__ __forceinline__ uint32_t window_bits(int p, int kb, int lo, int window, int sinks,
+                                                int w) {
+  const int top = p - kb + 1, low = lo - kb;
+  return bits_range(max(p - window + 1 - kb, low), top, w) |
+         bits_range(low, min(sinks - kb, top), w);
+}
+
+// One row over its visible keys, by a warp: fp32, key by key, online softmax.
+// Stops early once the whole row is NaN.
+template <typename T, int D>
+__device__ __noinline__ void window_row_slow(const WindowParams& p, int b, int head, int i) {
+  const int lane = threadIdx.x & 31;
+  const int pos = p.nkv - p.nq + i, kvh = head / p.g;
+  const T* q = static_cast<const T*>(p.q) + b * p.q_b + i * p.q_n + head * p.q_h;
+  const T* k = static_cast<const T*>(p.k) + b * p.k_b + kvh * p.k_h;
+  const T* v = static_cast<const T*>(p.v) + b * p.v_b + kvh * p.v_h;
+  float qr[D / 32], o[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    qr[c] = static_cast<float>(q[lane + 32 * c]);
+    o[c] = 0.f;
+  }
+  const int lo = max(0, pos - p.window + 1), ns = min(p.sinks, lo);
+  float m = -INFINITY, l = 0.f;
+  for (int u = 0; u < ns + pos + 1 - lo; ++u) {
+    const int j = u < ns ? u : lo + (u - ns);
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      s += qr[c] * static_cast<float>(k[j * p.k_n + lane + 32 * c]);
+    s = warp_sum(s) * p.scale_log2;
+    const float mn = fmaxf(m, s);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float alpha = exp2f(m - ref), w = exp2f(s - ref);
+    l = l * alpha + w;
+    m = mn;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      o[c] = o[c] * alpha + (w == 0.f ? 0.f : w * static_cast<float>(v[j * p.v_n + lane + 32 * c]));
+    if (l != l) break;
+  }
+  T* dst = static_cast<T*>(p.o) + b * p.o_b + i * p.o_n + head * p.o_h;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) dst[lane + 32 * c] = static_cast<T>(o[c] / l);
+}
+
+__device__ __forceinline__ void window_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void window_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void window_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                   taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
+
+// 16-column groups (of eight per row) whose exp2 runs as a cubic on the FMA
+// pipe, so that it shares the work of the exponential unit (unmasked tiles).
+constexpr uint32_t kWindowPolyGroups = 0x88u;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(384, 1)
+    attn_window_tc_kernel(const __grid_constant__ CUtensorMap mapQ,
+                          const __grid_constant__ CUtensorMap mapK,
+                          const __grid_constant__ CUtensorMap mapV, const WindowParams p) {
+  using C = WindowCfg<D>;
+  constexpr int kPerHand = 4 / C::HAND;  // 32-key chunks per hand-over
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  const uint32_t q_full = smem_u32(bars + 0);
+  const uint32_t ring_full0 = smem_u32(bars + 1);
+  const uint32_t ring_empty0 = smem_u32(bars + 1 + C::NSLOT);
+  const uint32_t s_full0 = smem_u32(bars + 1 + 2 * C::NSLOT);   // [A, B]
+  const uint32_t p_chunk0 = smem_u32(bars + 3 + 2 * C::NSLOT);  // [A: 0..3, B: 0..3]
+  const uint32_t o_done0 = smem_u32(bars + 11 + 2 * C::NSLOT);  // [A, B]
+  const uint32_t drain = smem_u32(bars + 13 + 2 * C::NSLOT);
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // within a (sequence, kv head): the last query blocks (most keys) first
+  const int bk = blockIdx.x / p.npairs;
+  const int pair = p.npairs - 1 - (static_cast<int>(blockIdx.x) - bk * p.npairs);
+  const int bidx = bk / p.hkv, kvh = bk - bidx * p.hkv;
+  const int len = window_len(p, bidx);
+  const int uA = 2 * pair, uB = 2 * pair + 1;
+  const bool has_b = uB < p.units;
+  const int qbA = uA / p.g, qbB = has_b ? uB / p.g : qbA;
+  const int headA = kvh * p.g + (uA - qbA * p.g);
+  const int headB = has_b ? kvh * p.g + (uB - qbB * p.g) : headA;
+  const WindowTile tA = window_tile(p, qbA, len), tB = window_tile(p, qbB, len);
+  const bool anyA = tA.any(), anyB = has_b && tB.any();
+  // (block A is never after block B: if A has no valid row, B has none)
+  const int lo = tA.lo, hi = anyB ? tB.hi : tA.hi;
+  const int ns = min(p.sinks, lo);
+  const int n_s = anyA ? (ns + 127) / 128 : 0;
+  const int n_w = anyA ? (hi - lo + 127) / 128 : 0;
+  const int n_kv = n_s + n_w;
+  const int w0 = hi - 128 * n_w;  // first key of the window tiles
+  // tiles seen by a query tile: the sink tiles and first .. last (sinks past
+  // lo lie in the window tiles, so there a tile starts at lo too)
+  auto first_of = [&](const WindowTile& t) {
+    return n_s + ((p.sinks > lo ? lo : t.lo) - w0) / 128;
+  };
+  auto last_of = [&](const WindowTile& t) { return n_s + (t.hi - 1 - w0) / 128; };
+  const int fA = first_of(tA), lA = last_of(tA);
+  const int fB = first_of(tB), lB = last_of(tB);
+  auto seen = [&](int x, int j) {
+    if (x == 0) return anyA && (j < n_s || (j >= fA && j <= lA));
+    return anyB && (j < n_s || (j >= fB && j <= lB));
+  };
+  auto key_of = [&](int j) { return j < n_s ? 128 * j : w0 + 128 * (j - n_s); };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::NSLOT; ++s) {
+      mbar_init(ring_full0 + 8 * s, 1);
+      mbar_init(ring_empty0 + 8 * s, 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full0 + 8 * x, 1);
+      for (int c = 0; c < 4; ++c) mbar_init(p_chunk0 + 8 * (4 * x + c), 4);
+      mbar_init(o_done0 + 8 * x, 1);
+    }
+    mbar_init(drain, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&tmem_base_sh), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort_flag = &abort_sh;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one();
+    int armed[C::NSLOT];
+    for (int s = 0; s < C::NSLOT; ++s) armed[s] = -1;
+    if (n_kv > 0) {
+      if (leader) {
+        mbar_arrive_expect_tx(q_full, C::TILE * (anyB ? 2 : 1));
+        tma_load_5d(smem_u32(smem), &mapQ, q_full, 0, qbA * 128, 0, headA, bidx);
+        if (anyB) tma_load_5d(smem_u32(smem + C::TILE), &mapQ, q_full, 0, qbB * 128, 0, headB, bidx);
+      }
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int j = 0; j < n_kv && ok; ++j) {
+        const int kb = key_of(j);
+        for (int w = 0; w < 2; ++w) {
+          if (!mbar_wait_warp(ring_empty0 + 8 * slot, phase ^ 1u, abort_flag, p.err,
+                              kSiteAttnProducer)) {
+            ok = false;
+            break;
+          }
+          armed[slot] = static_cast<int>(phase);
+          if (leader) {
+            mbar_arrive_expect_tx(ring_full0 + 8 * slot, C::TILE);
+            tma_load_5d(smem_u32(smem + C::OFF_RING + slot * C::TILE), w == 0 ? &mapK : &mapV,
+                        ring_full0 + 8 * slot, 0, kb, 0, kvh, bidx);
+          }
+          if (++slot == C::NSLOT) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      mbar_wait_drain(q_full, 0, p.err);
+      for (int s = 0; s < C::NSLOT; ++s)
+        if (armed[s] >= 0)
+          mbar_wait_drain(ring_full0 + 8 * s, static_cast<uint32_t>(armed[s]), p.err);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- UMMA issue
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = idesc16<T>(128, 128, false, false);
+    constexpr uint32_t idesc_o = idesc16<T>(128, D, false, true);
+    constexpr uint32_t hi_w = sdesc_hi(1024);
+    const uint32_t qa_lo = sdesc_lo(smem_u32(smem), 16);
+    const uint32_t qb_lo = sdesc_lo(smem_u32(smem + C::TILE), 16);
+    const uint32_t ring = smem_u32(smem + C::OFF_RING);
+    auto slot_of = [&](int t) { return t % C::NSLOT; };
+    auto phase_of = [&](int t) { return static_cast<uint32_t>((t / C::NSLOT) & 1); };
+    auto commit = [&](uint32_t bar) {
+      if (leader) umma_commit(bar);
+      __syncwarp();
+    };
+    auto issue_s = [&](int x, uint32_t k_lo) {
+      const uint32_t q_lo = x == 0 ? qa_lo : qb_lo, d_tmem = tmem + (x == 0 ? 0u : C::TM_S_B);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * C::CHUNK + (k & 3) * 32) >> 4;
+          umma_ss(d_tmem, q_lo + off, hi_w, k_lo + off, hi_w, idesc_s, k > 0 ? 1u : 0u);
+        }
+      }
+      __syncwarp();
+      commit(s_full0 + 8 * x);
+    };
+    uint32_t pph[2] = {0, 0};
+    bool o_started[2] = {false, false};
+    bool ok = n_kv > 0 && mbar_wait_warp(q_full, 0, abort_flag, p.err, kSiteAttnMma) &&
+              mbar_wait_warp(ring_full0, 0, abort_flag, p.err, kSiteAttnMma);
+    if (ok) {
+      tc_fence_after();
+      for (int x = 0; x < 2; ++x)
+        if (seen(x, 0)) issue_s(x, sdesc_lo(ring, 16));
+      commit(ring_empty0);
+    }
+    for (int j = 0; j < n_kv && ok; ++j) {
+      const int tv = 2 * j + 1, tk = 2 * j + 2;  // ring positions of V_j and K_j+1
+      if (!mbar_wait_warp(ring_full0 + 8 * slot_of(tv), phase_of(tv), abort_flag, p.err,
+                          kSiteAttnMma))
+        break;
+      bool k_ready = false;
+      const uint32_t v_lo = sdesc_lo(ring + slot_of(tv) * C::TILE, C::CHUNK);
+      const uint32_t k_lo = sdesc_lo(ring + slot_of(tk) * C::TILE, 16);
+      for (int x = 0; x < 2 && ok; ++x) {
+        const bool now = seen(x, j), next = j + 1 < n_kv && seen(x, j + 1);
+        if (now) {
+          const uint32_t tS = tmem + (x == 0 ? 0u : C::TM_S_B);
+          const uint32_t tO = tmem + (x == 0 ? C::TM_O_A : C::TM_O_B);
+          for (int hh = 0; hh < C::HAND; ++hh) {
+            if (!mbar_wait_warp(p_chunk0 + 8 * (4 * x + hh), pph[x], abort_flag, p.err,
+                                kSiteAttnMma)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int q = 0; q < 2 * kPerHand; ++q) {
+                const int k = 2 * hh * kPerHand + q;  // 16-key step
+                umma_ts(tO, tS + 8 * k, v_lo + ((k * 2048) >> 4), hi_w, idesc_o,
+                        (o_started[x] || k > 0) ? 1u : 0u);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          pph[x] ^= 1u;
+          o_started[x] = true;
+          if (j == (x == 0 ? lA : lB)) commit(o_done0 + 8 * x);
+        }
+        if (next) {
+          if (!k_ready) {
+            if (!mbar_wait_warp(ring_full0 + 8 * slot_of(tk), phase_of(tk), abort_flag, p.err,
+                                kSiteAttnMma)) {
+              ok = false;
+              break;
+            }
+            k_ready = true;
+          }
+          issue_s(x, k_lo);
+        }
+      }
+      if (!ok) break;
+      commit(ring_empty0 + 8 * slot_of(tv));
+      if (k_ready) commit(ring_empty0 + 8 * slot_of(tk));
+    }
+    commit(drain);
+    mbar_wait_drain(drain, 0, p.err);
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- softmax
+    const int x = (warp - 4) >> 2;  // 0: tile A, 1: tile B
+    const int e = warp & 3;         // TMEM lane quarter
+    const int r = e * 32 + lane;    // query row within the tile
+    const bool any = x == 0 ? anyA : anyB;
+    const int p0 = x == 0 ? tA.p0 : tB.p0;
+    const int first = x == 0 ? fA : fB, last = x == 0 ? lA : lB;
+    const int head = x == 0 ? headA : headB;
+    const int i = (x == 0 ? qbA : qbB) * 128 + r;
+    const int pos = p0 + r;
+    const bool in_q = i < p.nq && (x == 0 || has_b);
+    const bool valid = in_q && pos < len;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
+    const uint32_t tS = t_lane + (x == 0 ? 0u : C::TM_S_B);
+    const uint32_t tO = t_lane + (x == 0 ? C::TM_O_A : C::TM_O_B);
+    const uint32_t s_full = s_full0 + 8 * x;
+    const uint32_t p_chunk = p_chunk0 + 8 * (4 * x);
+    const float c = p.scale_log2;
+    float m_run = -INFINITY;   // reference maximum
+    float m_true = -INFINITY;  // the row's exact maximum
+    float l = 0.f;
+    bool o_live = false;
+    bool ok = any;
+    uint32_t ph = 0;
+    for (int j = n_s > 0 ? 0 : first; j <= last && ok; j = j + 1 == n_s ? first : j + 1) {
+      if (!mbar_wait_warp(s_full, ph, abort_flag, p.err, kSiteAttnSoftmax)) {
+        ok = false;
+        break;
+      }
+      ph ^= 1u;
+      tc_fence_after();
+      uint32_t sr[128];
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc)
+        tmem_ld_32x32b_x32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
+      tmem_ld_wait();
+      const int kb = key_of(j);
+      // a window tile that every row of the block sees whole
+      const bool full = j >= n_s && kb + 127 <= p0 && kb >= lo && kb >= p0 + 128 - p.window;
+      if (!full) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t vis = j < n_s ? bits_range(0, ns - kb, w)
+                                       : window_bits(pos, kb, lo, p.window, p.sinks, w);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!((vis >> k) & 1u)) sr[32 * w + k] = __float_as_uint(-INFINITY);
+        }
+      }
+      float mxp[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mxp[k] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 128; k += 16)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          mxp[q] = fmaxf(fmaxf(mxp[q], __uint_as_float(sr[k + q])), __uint_as_float(sr[k + 8 + q]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mxp[k] = fmaxf(mxp[k], mxp[k + 4]);
+      const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
+      m_true = fmaxf(m_true, mx);
+      float m_new = m_run;
+      bool need = false;
+      if (mx > m_run) {
+        need = (m_run == -INFINITY) || ((mx - m_run) * c > 8.0f);
+        if (need) m_new = mx;
+      }
+      const bool warp_need = __any_sync(0xffffffffu, need) && o_live;
+      const float alpha =
+          need ? (m_run == -INFINITY ? 0.f : ex2_approx((m_run - m_new) * c)) : 1.f;
+      if (warp_need) {
+#pragma unroll 1
+        for (int cc = 0; cc < D / 8; ++cc) {
+          uint32_t v[8];
+          window_ld8(tO + cc * 8, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+          window_st8(tO + cc * 8, v);
+        }
+      }
+      // a row that has seen no key yet keeps reference 0: exp2(-inf) = 0
+      const float ref = m_new == -INFINITY ? 0.f : -m_new * c;
+      const float2 cc2 = make_float2(c, c), mref2 = make_float2(ref, ref);
+      float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                        make_float2(0.f, 0.f)};
+      auto exp_row = [&](auto poly) {
+        constexpr uint32_t kMask = decltype(poly)::value;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const int col = cc * 32 + k;
+            const float2 a = __ffma2_rn(
+                make_float2(__uint_as_float(sr[col]), __uint_as_float(sr[col + 1])), cc2, mref2);
+            float2 e2;
+            if ((kMask >> (col >> 4)) & 1u)
+              e2 = exp2_poly2(a);
+            else
+              e2 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+            sum2[(k >> 1) & 3] = __fadd2_rn(sum2[(k >> 1) & 3], e2);
+            pk[k >> 1] = pack16<T>(e2.x, e2.y);
+          }
+          window_st16(tS + cc * 16, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && (cc + 1) % kPerHand == 0) mbar_arrive(p_chunk + 8 * (cc / kPerHand));
+        }
+      };
+      if (full)
+        exp_row(std::integral_constant<uint32_t, kWindowPolyGroups>{});
+      else
+        exp_row(std::integral_constant<uint32_t, 0u>{});
+      sum2[0] = __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
+      l = alpha * l + (sum2[0].x + sum2[0].y);
+      m_run = m_new;
+      o_live = true;
+    }
+    if (ok) ok = mbar_wait_warp(o_done0 + 8 * x, 0, abort_flag, p.err, kSiteAttnSoftmax);
+    if (ok || !any) {
+      tc_fence_after();
+      const float inv_l = valid ? 1.0f / l : 0.f;
+      if (p.stats != nullptr && in_q) {
+        // in the units of s = q.k / sqrt(d_k): m the exact maximum, l relative to it
+        const float m_s = m_true * c * 0.69314718055994531f;
+        const float l_s = l * ex2_approx((m_run - m_true) * c);
+        p.stats[(static_cast<long long>(bidx) * p.h + head) * p.nq + i] =
+            valid ? make_float2(m_s, l_s) : make_float2(-INFINITY, 0.f);
+      }
+      T* dst = static_cast<T*>(p.o) + bidx * p.o_b + i * p.o_n + head * p.o_h;
+      float odd = 0.f;  // becomes NaN if an output is not finite
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t v[32];
+        if (any) {
+          tmem_ld_32x32b_x32(tO + cc * 32, v);
+          tmem_ld_wait();
+        }
+        if (!in_q) continue;
+        uint4* d4 = reinterpret_cast<uint4*>(dst + cc * 32);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float(v[q * 8 + 2 * k]) * inv_l;
+            const float b = __uint_as_float(v[q * 8 + 2 * k + 1]) * inv_l;
+            odd = fmaf(a, 0.f, fmaf(b, 0.f, odd));
+            w[k] = valid ? pack16<T>(a, b) : 0u;
+          }
+          d4[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      uint32_t again = __ballot_sync(0xffffffffu, valid && odd != 0.f);
+      if (again) {
+        __syncwarp();
+        for (; again; again &= again - 1) {
+          const int rr = __ffs(again) - 1;
+          window_row_slow<T, D>(p, bidx, head, i - lane + rr);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+}  // namespace bpt

@@ -21,6 +21,7 @@
 // the namespace gets its own name, so that both units link into one library.
 #define bpt bpt_ops
 #include "attn_decode.cuh"
+#include "attn_window_tc.cuh"
 #include "cache.cuh"
 #include "common.cuh"
 
@@ -83,7 +84,11 @@ bpt_status ops_device(int* sms) {
         (smem_fails(bpt::attn_decode_split_kernel<bf, 64>, bpt::DecodeCfg<64>::SMEM) ||
          smem_fails(bpt::attn_decode_split_kernel<bf, 128>, bpt::DecodeCfg<128>::SMEM) ||
          smem_fails(bpt::attn_decode_split_kernel<__half, 64>, bpt::DecodeCfg<64>::SMEM) ||
-         smem_fails(bpt::attn_decode_split_kernel<__half, 128>, bpt::DecodeCfg<128>::SMEM)))
+         smem_fails(bpt::attn_decode_split_kernel<__half, 128>, bpt::DecodeCfg<128>::SMEM) ||
+         smem_fails(bpt::attn_window_tc_kernel<bf, 64>, bpt::WindowCfg<64>::SMEM) ||
+         smem_fails(bpt::attn_window_tc_kernel<bf, 128>, bpt::WindowCfg<128>::SMEM) ||
+         smem_fails(bpt::attn_window_tc_kernel<__half, 64>, bpt::WindowCfg<64>::SMEM) ||
+         smem_fails(bpt::attn_window_tc_kernel<__half, 128>, bpt::WindowCfg<128>::SMEM)))
       return BPT_ERR_CUDA;
     d.init = true;
   }
@@ -186,6 +191,93 @@ cudaError_t launch_decode(const bpt::DecodeParams& p, unsigned slot_blocks, cuda
   if (e != cudaSuccess) return e;
   bpt::attn_decode_join_kernel<T, D>
       <<<dim3(p.B * p.c.hkv, 1 + slot_blocks), bpt::kJoinThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ window --
+PFN_cuTensorMapEncodeTiled_v12000 g_ops_encode = nullptr;
+
+bpt_status ops_encoder() {
+  std::lock_guard<std::mutex> lk(g_ops_mu);
+  if (g_ops_encode) return BPT_OK;
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) !=
+          cudaSuccess ||
+      q != cudaDriverEntryPointSuccess || fn == nullptr)
+    return BPT_ERR_CUDA;
+  g_ops_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  return BPT_OK;
+}
+
+// Strided rows [batch, n, heads, d_k] viewed as [batch][heads][d_k/64][n][64]:
+// a box is 128 rows of one head, 64-column chunks one after another in shared
+// memory (128-byte swizzle).  Rows outside 0 .. n-1 read as zeros.
+bool map_rows(CUtensorMap* m, const bpt_rows& r, int64_t batch, int64_t n, int64_t heads,
+              int64_t dk) {
+  const int64_t any = 128;  // the stride of a dimension of one entry is not used
+  cuuint64_t dims[5] = {64, cuuint64_t(n), cuuint64_t(dk / 64), cuuint64_t(heads),
+                        cuuint64_t(batch)};
+  cuuint64_t st[4] = {cuuint64_t(n > 1 ? r.stride_n * 2 : any), 128,
+                      cuuint64_t(heads > 1 ? r.stride_h * 2 : any),
+                      cuuint64_t(batch > 1 ? r.stride_b * 2 : any)};
+  cuuint32_t box[5] = {64, 128, cuuint32_t(dk / 64), 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return g_ops_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, r.data, dims, st, box, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bpt_status check_window(const bpt_window* w) {
+  if (w == nullptr) return BPT_ERR_INVALID_ARG;
+  if (w->dtype != BPT_BF16 && w->dtype != BPT_F16) return BPT_ERR_INVALID_ARG;
+  if (w->reserved != 0 || w->batch < 0 || w->n_q < 0 || w->n_kv < 0 || w->heads <= 0 ||
+      w->kv_heads <= 0 || w->heads % w->kv_heads != 0 || w->n_q > w->n_kv || w->window <= 0 ||
+      w->sinks < 0)
+    return BPT_ERR_INVALID_ARG;
+  if (w->d_k != 64 && w->d_k != 128) return BPT_ERR_UNSUPPORTED;
+  const int64_t lim = int64_t(1) << 30;
+  if (w->n_kv > lim || w->heads > lim || w->batch > lim) return BPT_ERR_UNSUPPORTED;
+  // CTAs of a launch (a 31-bit grid), one per two query tiles at most
+  const int64_t tiles = (w->n_kv + 127) / 128, hb = w->heads * std::max<int64_t>(1, w->batch);
+  if (hb >= lim || tiles >= (int64_t(1) << 31) / hb) return BPT_ERR_UNSUPPORTED;
+  return BPT_OK;
+}
+
+// A strided 16-bit tensor the kernels may read: 16-byte rows, positive
+// strides (a broadcast dimension has to be materialised).
+bool rows_ok(const bpt_rows& r, int64_t batch, int64_t n, int64_t heads) {
+  if (r.data == nullptr || unaligned(r.data, 16)) return false;
+  const std::pair<int64_t, int64_t> dims[3] = {
+      {batch, r.stride_b}, {n, r.stride_n}, {heads, r.stride_h}};
+  for (const auto& d : dims)
+    if (d.first > 1 && (d.second <= 0 || d.second % 8 != 0 || d.second >= (int64_t(1) << 38)))
+      return false;
+  return true;
+}
+Range rows_range(const bpt_rows& r, int64_t batch, int64_t n, int64_t heads, int64_t dk) {
+  return Range(r.data, extent({{batch, r.stride_b}, {n, r.stride_n}, {heads, r.stride_h}}, dk));
+}
+// Written rows must not meet one another: ordered by stride, each dimension
+// steps past the extent of the smaller ones.
+bool rows_apart(const bpt_rows& r, int64_t batch, int64_t n, int64_t heads, int64_t dk) {
+  std::pair<int64_t, int64_t> d[3] = {{r.stride_b, batch}, {r.stride_n, n}, {r.stride_h, heads}};
+  std::sort(d, d + 3);
+  int64_t ext = dk;
+  for (const auto& x : d)
+    if (x.second > 1) {
+      if (x.first < ext) return false;
+      ext += x.first * (x.second - 1);
+    }
+  return true;
+}
+
+template <typename T, int D>
+cudaError_t launch_window(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                          const bpt::WindowParams& p, int64_t batch, cudaStream_t s) {
+  using C = bpt::WindowCfg<D>;
+  bpt::attn_window_tc_kernel<T, D>
+      <<<unsigned(batch * p.hkv * p.npairs), C::THREADS, C::SMEM, s>>>(q, k, v, p);
   return cudaGetLastError();
 }
 
@@ -417,6 +509,78 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
   else
     e = dk == 128 ? launch_decode<__half, 128>(p, slot_blocks, s)
                   : launch_decode<__half, 64>(p, slot_blocks, s);
+  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status bpt_attn_window_workspace_size(const bpt_window* w, size_t* bytes) {
+  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
+  const bpt_status st = check_window(w);
+  if (st != BPT_OK) return st;
+  *bytes = kOpsHeader;
+  return BPT_OK;
+}
+
+bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
+                                   const bpt_rows* v, const int32_t* lens, const bpt_rows* out,
+                                   float* stats, void* workspace, size_t workspace_bytes,
+                                   bpt_stream_t stream) {
+  bpt_status st = check_window(w);
+  if (st != BPT_OK) return st;
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr) return BPT_ERR_INVALID_ARG;
+  if (w->batch == 0 || w->n_q == 0) return BPT_OK;
+  const int64_t B = w->batch, nq = w->n_q, nkv = w->n_kv, h = w->heads, hkv = w->kv_heads,
+                dk = w->d_k;
+  if (!rows_ok(*q, B, nq, h) || !rows_ok(*k, B, nkv, hkv) || !rows_ok(*v, B, nkv, hkv) ||
+      !rows_ok(*out, B, nq, h) || !rows_apart(*out, B, nq, h, dk) || unaligned(lens, 4) ||
+      unaligned(stats, 8) || workspace == nullptr || unaligned(workspace, 256))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace_bytes < kOpsHeader) return BPT_ERR_WORKSPACE;
+  const Range rq = rows_range(*q, B, nq, h, dk), rk = rows_range(*k, B, nkv, hkv, dk),
+              rv = rows_range(*v, B, nkv, hkv, dk), rl(lens, size_t(B) * 4),
+              rs(stats, size_t(B * h) * size_t(nq) * 8), rw(workspace, kOpsHeader);
+  const Range ro = rows_range(*out, B, nq, h, dk);
+  if (any_meets(ro, {rq, rk, rv, rl, rs, rw}) || any_meets(rs, {rq, rk, rv, rl, rw}) ||
+      any_meets(rw, {rq, rk, rv, rl}))
+    return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  st = ops_encoder();
+  if (st != BPT_OK) return st;
+  CUtensorMap mq, mk, mv;
+  if (!map_rows(&mq, *q, B, nq, h, dk) || !map_rows(&mk, *k, B, nkv, hkv, dk) ||
+      !map_rows(&mv, *v, B, nkv, hkv, dk))
+    return BPT_ERR_CUDA;
+  bpt::WindowParams p{};
+  p.nq = int(nq);
+  p.nkv = int(nkv);
+  p.h = int(h);
+  p.hkv = int(hkv);
+  p.g = int(h / hkv);
+  p.units = int((nq + 127) / 128) * p.g;
+  p.npairs = (p.units + 1) / 2;
+  p.window = int(std::min<int64_t>(w->window, nkv));
+  p.sinks = int(std::min<int64_t>(w->sinks, nkv));
+  p.lens = lens;
+  p.q = q->data;
+  p.k = k->data;
+  p.v = v->data;
+  p.q_b = q->stride_b; p.q_n = q->stride_n; p.q_h = q->stride_h;
+  p.k_b = k->stride_b; p.k_n = k->stride_n; p.k_h = k->stride_h;
+  p.v_b = v->stride_b; p.v_n = v->stride_n; p.v_h = v->stride_h;
+  p.o = out->data;
+  p.o_b = out->stride_b; p.o_n = out->stride_n; p.o_h = out->stride_h;
+  p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
+  p.stats = reinterpret_cast<float2*>(stats);
+  p.err = static_cast<uint32_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (w->dtype == BPT_BF16)
+    e = dk == 128 ? launch_window<__nv_bfloat16, 128>(mq, mk, mv, p, B, s)
+                  : launch_window<__nv_bfloat16, 64>(mq, mk, mv, p, B, s);
+  else
+    e = dk == 128 ? launch_window<__half, 128>(mq, mk, mv, p, B, s)
+                  : launch_window<__half, 64>(mq, mk, mv, p, B, s);
   return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
 

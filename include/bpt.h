@@ -696,6 +696,59 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
                            int64_t out_stride_h, void* workspace, size_t workspace_bytes,
                            bpt_stream_t stream);
 
+/* ------------------------------------- attention with a sliding window --
+ * Exact softmax attention of n_q queries over n_kv >= n_q keys under a causal
+ * sliding window with sinks (first tokens that stay visible).  Query i stands
+ * at position p = n_kv - n_q + i of its sequence (n_q = n_kv: whole sequences;
+ * n_q < n_kv: a chunk behind a prefix whose keys are already there) and sees
+ * key j if
+ *     j <= p  and  p < lens[b]  and  (p - j < window or j < sinks).
+ * window >= n_kv is plain causal attention.  kv_heads divides heads, head t
+ * reads kv head t / (heads / kv_heads).  lens (nullable, [batch], on the
+ * device): tokens of each sequence; rows at positions >= lens[b] give o = 0.
+ * A length outside 0 .. n_kv is taken as the nearest of the two and
+ * BPT_ERR_INDEX is recorded.
+ *
+ * Tensors are strided (element strides, positive multiples of 8; 16-byte
+ * aligned; the d_k = 64 or 128 elements of a row contiguous), bf16 or fp16:
+ * the three parts of a packed projection can be given as they lie.  A
+ * broadcast dimension (stride 0) is refused with BPT_ERR_INVALID_ARG.
+ *
+ * Only what a row sees counts: NaN and infinities in keys and values that it
+ * does not see (masked ones, padding) do not reach its output.
+ *
+ * Workspaces: as for the cache's operators (first 256 bytes zeroed once by
+ * the caller; one per call that may overlap with another).
+ */
+typedef struct {
+  int64_t batch, n_q, n_kv, heads, kv_heads, d_k;
+  int64_t window; /* > 0 */
+  int64_t sinks;  /* >= 0 */
+  int32_t dtype;  /* BPT_BF16 or BPT_F16 */
+  int32_t reserved; /* 0 */
+} bpt_window;
+
+/* Rows of d_k 16-bit elements: element (b, i, t, c) at
+ * data + b stride_b + i stride_n + t stride_h + c. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_n, stride_h;
+} bpt_rows;
+
+bpt_status bpt_attn_window_workspace_size(const bpt_window* w, size_t* bytes);
+
+/*
+ * bpt_attn_window_forward -- out [batch, n_q, heads, d_k] = the attention of
+ * q [batch, n_q, heads, d_k] over k, v [batch, n_kv, kv_heads, d_k].
+ * stats (nullable): fp32 [batch, heads, n_q, 2], per row m = the maximum of
+ * q . k_j / sqrt(d_k) over the keys it sees and l = sum exp(s_j - m); rows
+ * past the length get (-inf, 0).  out may not overlap any input.
+ */
+bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
+                                   const bpt_rows* v, const int32_t* lens, const bpt_rows* out,
+                                   float* stats, void* workspace, size_t workspace_bytes,
+                                   bpt_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
