@@ -10,7 +10,8 @@ from ._lib import (  # noqa: F401
     BPT_ERR_WORKSPACE, BPT_F16, BPT_F32, BPT_OK, BPT_SCHEDULE_FUSED, BPT_SCHEDULE_WAVES,
     BPT_STATIC_WORKSPACE_BYTES, BPT_TAIL_MAX_PAIRS, BPT_WAVE_BLOCKS, EXPORTED, KINDS, LIB_PATH,
     BptError, Cache, Options, Rows, Window, bpt_attn_decode, bpt_attn_decode_workspace_size,
-    bpt_attn_window_forward, bpt_attn_window_workspace_size, bpt_cache_append,
+    bpt_attn_window_backward, bpt_attn_window_backward_workspace_size, bpt_attn_window_forward,
+    bpt_attn_window_workspace_size, bpt_cache_append,
     bpt_cache_evict, bpt_cache_workspace_size, bpt_layer_backward, bpt_layer_backward_keep_o, bpt_layer_backward_opt,
     bpt_layer_backward_workspace_size, bpt_layer_backward_workspace_size_opt,
     bpt_layer_forward, bpt_layer_forward_bsfa, bpt_layer_forward_bsfa_opt, bpt_layer_forward_opt,
@@ -22,7 +23,10 @@ from ._lib import (  # noqa: F401
     bpt_profile_enable, bpt_profile_read, bpt_read_device_error, bpt_status_string, load,
     make_options, status_string,
 )
-from .attn import attn_window_forward, attn_window_workspace  # noqa: F401
+from .attn import (  # noqa: F401
+    attn_window_backward, attn_window_backward_workspace, attn_window_forward,
+    attn_window_workspace,
+)
 from .cache import (  # noqa: F401
     attn_decode, attn_decode_workspace, cache_append, cache_evict, cache_workspace,
 )

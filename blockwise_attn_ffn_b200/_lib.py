@@ -39,6 +39,7 @@ EXPORTED = [
     "bpt_cache_workspace_size", "bpt_cache_append", "bpt_cache_evict",
     "bpt_attn_decode_workspace_size", "bpt_attn_decode",
     "bpt_attn_window_workspace_size", "bpt_attn_window_forward",
+    "bpt_attn_window_backward_workspace_size", "bpt_attn_window_backward",
 ]
 
 
@@ -188,9 +189,13 @@ def load() -> ctypes.CDLL:
     pw, pr = ctypes.POINTER(Window), ctypes.POINTER(Rows)
     lib.bpt_attn_window_workspace_size.argtypes = [pw, pz]
     lib.bpt_attn_window_forward.argtypes = [pw, pr, pr, pr, vp, pr, vp, vp, sz, vp]
+    lib.bpt_attn_window_backward_workspace_size.argtypes = [pw, pz]
+    lib.bpt_attn_window_backward.argtypes = [pw, pr, pr, pr, pr, vp, pr, vp, pr, pr, pr, vp, sz,
+                                             vp]
     for fn in (lib.bpt_cache_workspace_size, lib.bpt_cache_append, lib.bpt_cache_evict,
                lib.bpt_attn_decode_workspace_size, lib.bpt_attn_decode,
-               lib.bpt_attn_window_workspace_size, lib.bpt_attn_window_forward):
+               lib.bpt_attn_window_workspace_size, lib.bpt_attn_window_forward,
+               lib.bpt_attn_window_backward_workspace_size, lib.bpt_attn_window_backward):
         fn.restype = i32
     _lib = lib
     return lib
@@ -461,3 +466,17 @@ def bpt_attn_window_forward(window, q, k, v, lens, out, stats, workspace, worksp
     """Pointer-level call (lens, stats may be None); returns the status."""
     return load().bpt_attn_window_forward(window, q, k, v, lens, out, stats, workspace,
                                           workspace_bytes, stream)
+
+
+def bpt_attn_window_backward_workspace_size(window: Window) -> Tuple[int, int]:
+    """Returns (status, bytes)."""
+    out = ctypes.c_size_t(0)
+    st = load().bpt_attn_window_backward_workspace_size(ctypes.byref(window), ctypes.byref(out))
+    return st, out.value
+
+
+def bpt_attn_window_backward(window, q, k, v, o, stats, d_o, lens, dq, dk, dv, workspace,
+                             workspace_bytes, stream) -> int:
+    """Pointer-level call (lens may be None); returns the status."""
+    return load().bpt_attn_window_backward(window, q, k, v, o, stats, d_o, lens, dq, dk, dv,
+                                           workspace, workspace_bytes, stream)

@@ -1,0 +1,909 @@
+// Gradients of attention with a sliding window and sinks on the tcgen05
+// tensor cores (the forward and its visibility rule: attn_window_tc.cuh).
+//
+// With s = q.k / sqrt(d_k), P = exp(s - m) / l from the forward's (m, l) and
+// D = rowsum(dO * O), per head:
+//   dP = dO V^T,  dS = P * (dP - D),
+//   dV = P^T dO,  dK = dS^T Q / sqrt(d_k),  dQ = dS K / sqrt(d_k);
+// dK and dV sum over the query heads that share a kv head.
+//
+// Four launches, all sums in a fixed order (no atomics on results):
+//   window_terms_kernel   per row a' = -(m + ln l) log2 e and -D (reads o, dO
+//                         once); for fp16 also max |dO|.
+//   window_dkv_tc_kernel  one CTA per 128 keys of a kv head (or a part of
+//                         their queries): K, V stay, the (query head, query
+//                         tile) pairs that see them stream through.
+//   window_join_kernel    adds the parts of blocks that were cut.
+//   window_dq_tc_kernel   one CTA per 128 queries of a head: Q, dO stay, the
+//                         key tiles that they see stream through.
+// The tensor cores bound both big kernels (7 products of 2 d_k flops per pair
+// for the 5 of the formulas: S and dP are computed twice, which costs less
+// than adding dQ tiles up through memory and keeps results independent of
+// timing).
+//
+// Query tiles of a key block END at the last valid query that sees it, key
+// tiles of a query block at its last visible key: nothing past a sequence's
+// length is multiplied, so padding may hold anything.
+//
+// Key blocks that hold sinks are seen by every later query.  The (head, tile)
+// items of a block are cut into parts of at most `part_len`, which is half of
+// what an SM does in all, so that no CTA outlasts the rest; parts write fp32
+// accumulators and the join adds them in order.
+//
+// Rounding: P and dS are rounded to the operands' type for the products.
+// fp16 has 5 exponent bits, so there both are scaled by powers of two (exact):
+// P by 2^8, dS by 2^4 over max |dO| (its exponent), which keeps weights down
+// to 2^-22 and gradients 2^-40 below the largest out of the subnormals.
+#pragma once
+
+#include <type_traits>
+
+#include "attn_bwd_tc.cuh"
+#include "attn_window_tc.cuh"
+
+namespace bpt {
+
+constexpr int kWinBwdThreads = 384;  // TMA, UMMA, TMEM owner, idle; 8 elementwise warps
+// 16-column groups (of eight) whose exp2 runs on the FMA pipe (unmasked tiles)
+constexpr uint32_t kWinBwdPolyGroups = 0x88u;
+
+struct WindowBwdParams {
+  int nq, nkv, h, hkv, g, nqb, nblk;
+  int window, sinks;
+  const int* lens;        // nullable [B]
+  const float2* terms;    // [B][h][nq]: (a', -D); (-inf, 0) past the length
+  const uint32_t* amax;   // fp16: bits of max |dO|; null: bf16
+  void* dq;
+  long long dq_b, dq_n, dq_h;
+  void* dk;
+  long long dk_b, dk_n, dk_h;
+  void* dv;
+  long long dv_b, dv_n, dv_h;
+  float scale;            // 1 / sqrt(d_k)
+  int part_len;           // items per part
+  int split_parts;        // parts of cut blocks per (sequence, kv head)
+  float* part;            // [B * hkv][split_parts][2][128][d_k]: dV, dK
+  uint32_t* err;
+};
+
+// Query tiles that see the 128 keys from kb, of queries before row `limit`.
+struct WindowQueries {
+  int start, end;  // rows; tiles end at `end`
+  __host__ __device__ int tiles() const { return end > start ? (end - start + 127) / 128 : 0; }
+};
+__host__ __device__ inline WindowQueries window_queries(int nq, int nkv, int window, int sinks,
+                                                        int kb, int limit) {
+  const int off = nkv - nq;
+  WindowQueries q;
+  q.start = kb > off ? kb - off : 0;
+  q.end = nq;
+  if (kb >= sinks && kb + 127 + window - off < nq) q.end = kb + 127 + window - off;
+  if (limit < q.end) q.end = limit;
+  return q;
+}
+__host__ __device__ inline int window_parts(int nq, int nkv, int window, int sinks, int g, int kb,
+                                            int part_len) {
+  const int n = g * window_queries(nq, nkv, window, sinks, kb, nq).tiles();
+  return n <= part_len ? 1 : (n + part_len - 1) / part_len;
+}
+
+template <typename T>
+struct WinScale {
+  static constexpr float kP = std::is_same<T, __half>::value ? 8.f : 0.f;     // log2 of P's scale
+  static constexpr float kDS = std::is_same<T, __half>::value ? 16.f : 1.f;   // dS's, over max |dO|
+};
+// 2^-e with max |dO| in [2^e, 2^(e+1)); 1 where that is no use.
+__device__ __forceinline__ float grad_sigma(const uint32_t* amax) {
+  if (amax == nullptr) return 1.f;
+  const uint32_t e = __ldg(amax) >> 23;  // biased exponent (the sign is 0)
+  if (e == 0 || e >= 250) return 1.f;
+  return __uint_as_float((254u - e) << 23);
+}
+
+// ------------------------------------------------------------------- terms --
+struct WindowTermsParams {
+  const void* o;
+  long long o_b, o_n, o_h;
+  const void* d_o;
+  long long d_b, d_n, d_h;
+  const float2* stats;  // [B][h][nq]
+  float2* terms;
+  uint32_t* amax;       // nullable
+  const int* lens;
+  int B, nq, nkv, h;
+  uint32_t* err;
+};
+
+// D / 8 lanes per row (16 bytes of o and dO each), rows in (b, i, head) order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) window_terms_kernel(const WindowTermsParams p) {
+  constexpr int kLanes = D / 8;
+  const long long rows = static_cast<long long>(p.B) * p.nq * p.h;
+  const long long r = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  float sum = 0.f, mx = 0.f;
+  int b = 0, i = 0, t = 0;
+  bool valid = false;
+  if (r < rows) {
+    const long long bi = r / p.h;
+    t = static_cast<int>(r - bi * p.h);
+    b = static_cast<int>(bi / p.nq);
+    i = static_cast<int>(bi - static_cast<long long>(b) * p.nq);
+    int len = p.lens != nullptr ? __ldg(p.lens + b) : p.nkv;
+    if (len < 0 || len > p.nkv) {
+      record_error(p.err, kErrIndex, kSiteWindowLens);
+      len = len < 0 ? 0 : p.nkv;
+    }
+    valid = p.nkv - p.nq + i < len;
+    if (valid) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) +
+                                                           b * p.o_b + i * p.o_n + t * p.o_h) + lane);
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.d_o) +
+                                                           b * p.d_b + i * p.d_n + t * p.d_h) + lane);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = unpack16<T>(aw[k]), y = unpack16<T>(cw[k]);
+        sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+        mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
+      }
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (r < rows && lane == 0) {
+    const long long at = (static_cast<long long>(b) * p.h + t) * p.nq + i;
+    const float2 ml = p.stats[at];
+    p.terms[at] = valid && ml.y > 0.f
+                      ? make_float2(-(ml.x + logf(ml.y)) * kLog2e + WinScale<T>::kP, -sum)
+                      : make_float2(-INFINITY, 0.f);
+  }
+  if (p.amax != nullptr) {
+    __shared__ uint32_t mx_sh[8];
+    const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+    if ((threadIdx.x & 31) == 0) mx_sh[threadIdx.x >> 5] = w;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t m = 0;
+      for (int k = 0; k < 8; ++k) m = max(m, mx_sh[k]);
+      if (m != 0) atomicMax(p.amax, m);  // a maximum: the same in any order
+    }
+  }
+}
+
+// --------------------------------------------------------- elementwise parts --
+// P of 32 columns (fp16 / bf16 pairs) from the scores: 2^(S c + a), a per
+// column pair from `col` or one for the row.
+template <typename T, uint32_t POLY, typename F>
+__device__ __forceinline__ void win_p32(const uint32_t (&sr)[32], uint32_t* pp, float c, F&& term,
+                                        int cc, uint32_t vis, bool masked) {
+  const float2 c2 = make_float2(c, c);
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const float2 x =
+        __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, term(k));
+    float2 e;
+    if constexpr (POLY != 0) {
+      if ((POLY >> (2 * cc + (k >> 4))) & 1u)
+        e = exp2_poly2(x);
+      else
+        e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    } else {
+      e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      if (masked) {
+        if (!((vis >> k) & 1u)) e.x = 0.f;
+        if (!((vis >> (k + 1)) & 1u)) e.y = 0.f;
+      }
+    }
+    pp[k >> 1] = pack16<T>(e.x, e.y);
+  }
+}
+// dS = P (dP sig + nd) of 32 columns.
+template <typename T, bool MASKED, typename F>
+__device__ __forceinline__ void win_ds32(const uint32_t (&dr)[32], const uint32_t* pp, uint32_t* ds,
+                                         float sig, F&& nd, uint32_t vis) {
+  const float2 s2 = make_float2(sig, sig);
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    float2 v = __fmul2_rn(
+        unpack16<T>(pp[k >> 1]),
+        __ffma2_rn(make_float2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1])), s2, nd(k)));
+    if constexpr (MASKED) {  // 0 x (a value that is not finite) is not 0
+      if (!((vis >> k) & 1u)) v.x = 0.f;
+      if (!((vis >> (k + 1)) & 1u)) v.y = 0.f;
+    }
+    ds[k >> 1] = pack16<T>(v.x, v.y);
+  }
+}
+
+__device__ __forceinline__ void elementwise_sync() {
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+template <int D>
+struct WindowBwdCfg {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int CHUNK = 128 * 128;
+  // dK/dV: K, V, a ring of (Q, dO), two buffers of row terms
+  static constexpr int KV_SLOTS = D == 128 ? 2 : 4;
+  static constexpr int KV_OFF_RING = 2 * TILE;
+  static constexpr int KV_OFF_TERMS = KV_OFF_RING + KV_SLOTS * 2 * TILE;
+  static constexpr int KV_OFF_BAR = KV_OFF_TERMS + 2 * 2 * 128 * 4;
+  static constexpr int KV_SMEM = KV_OFF_BAR + 256 + 1024;
+  // dQ: Q, dO, rings of K (held until dQ_j) and V (until dP_j)
+  static constexpr int QK_SLOTS = 3, QV_SLOTS = 2;
+  static constexpr int Q_OFF_K = 2 * TILE;
+  static constexpr int Q_OFF_V = Q_OFF_K + QK_SLOTS * TILE;
+  static constexpr int Q_OFF_BAR = Q_OFF_V + QV_SLOTS * TILE;
+  static constexpr int Q_SMEM = Q_OFF_BAR + 256 + 1024;
+  static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D;
+  static constexpr uint32_t TQ_S = 0, TQ_DP = 256, TQ_A = 384;
+  static_assert(KV_SMEM <= 232448 && Q_SMEM <= 232448, "shared memory");
+};
+
+// A 128-row product with A from tensor memory, the two 32-column chunks of
+// one half of A's columns.
+template <int D>
+__device__ __forceinline__ void win_issue_ts_half(uint32_t d, uint32_t a, uint32_t b_lo,
+                                                  uint32_t idesc, int half, bool first) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) bwd_issue_ts_chunk<D>(d, a, b_lo, idesc, 2 * half + q, first);
+}
+
+// Eight consecutive values of a row as 16 bytes.
+template <typename T>
+__device__ __forceinline__ uint4 win_pack8(const uint32_t* v, float f) {
+  return make_uint4(pack16<T>(__uint_as_float(v[0]) * f, __uint_as_float(v[1]) * f),
+                    pack16<T>(__uint_as_float(v[2]) * f, __uint_as_float(v[3]) * f),
+                    pack16<T>(__uint_as_float(v[4]) * f, __uint_as_float(v[5]) * f),
+                    pack16<T>(__uint_as_float(v[6]) * f, __uint_as_float(v[7]) * f));
+}
+
+// ------------------------------------------------------------------ dK, dV --
+// Grid (parts of one (sequence, kv head), B * hkv).
+template <typename T, int D>
+__global__ void __launch_bounds__(kWinBwdThreads, 1)
+    window_dkv_tc_kernel(const __grid_constant__ CUtensorMap mapQ,
+                         const __grid_constant__ CUtensorMap mapK,
+                         const __grid_constant__ CUtensorMap mapV,
+                         const __grid_constant__ CUtensorMap mapDO, const WindowBwdParams p) {
+  using C = WindowBwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::KV_OFF_BAR);
+  const uint32_t kv_full = smem_u32(bars + 0);
+  const uint32_t ring_full0 = smem_u32(bars + 1);
+  const uint32_t ring_empty0 = smem_u32(bars + 5);
+  const uint32_t s_full = smem_u32(bars + 9);
+  const uint32_t dp_full = smem_u32(bars + 10);
+  const uint32_t p_half0 = smem_u32(bars + 11);   // [2]
+  const uint32_t ds_half0 = smem_u32(bars + 13);  // [2]
+  const uint32_t acc_done = smem_u32(bars + 15);
+  const uint32_t drain = smem_u32(bars + 16);
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  __shared__ int plan_sh[3];  // key block, part, first slot of its parts (-1: not cut)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bk = blockIdx.y;
+  const int bidx = bk / p.hkv, kvh = bk - bidx * p.hkv;
+  const int off = p.nkv - p.nq;
+  int len = p.lens != nullptr ? __ldg(p.lens + bidx) : p.nkv;
+  len = min(max(len, 0), p.nkv);
+
+  if (warp == 3) {
+    // the key block and part of this CTA: 32 blocks' parts at a time
+    int at = 0, slot = 0;
+    for (int b0 = 0; b0 < p.nblk; b0 += 32) {
+      const int blk = b0 + lane;
+      const int n = blk < p.nblk ? window_parts(p.nq, p.nkv, p.window, p.sinks, p.g, blk * 128,
+                                                p.part_len)
+                                 : 0;
+      int inc = n, sinc = n > 1 ? n : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, inc, o), c = __shfl_up_sync(0xffffffffu, sinc, o);
+        if (lane >= o) {
+          inc += a;
+          sinc += c;
+        }
+      }
+      const int first = at + inc - n, x = static_cast<int>(blockIdx.x);
+      if (x >= first && x < first + n) {
+        plan_sh[0] = blk;
+        plan_sh[1] = x - first;
+        plan_sh[2] = n > 1 ? slot + sinc - n : -1;
+      }
+      at += __shfl_sync(0xffffffffu, inc, 31);
+      slot += __shfl_sync(0xffffffffu, sinc, 31);
+      if (x < at) break;
+    }
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < C::KV_SLOTS; ++s) {
+      mbar_init(ring_full0 + 8 * s, 1);
+      mbar_init(ring_empty0 + 8 * s, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(p_half0 + 8 * c, 4);
+      mbar_init(ds_half0 + 8 * c, 4);
+    }
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&tmem_base_sh), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort_flag = &abort_sh;
+  const int jb = plan_sh[0], part = plan_sh[1], slot0 = plan_sh[2];
+  const int kb = jb * 128;
+  const WindowQueries wq = window_queries(p.nq, p.nkv, p.window, p.sinks, kb, len - off);
+  const int tiles = wq.tiles();
+  const int it0 = slot0 < 0 ? 0 : part * p.part_len;
+  const int it1 = slot0 < 0 ? p.g * tiles : min(p.g * tiles, it0 + p.part_len);
+  const int n_it = max(0, it1 - it0);
+  // (head of the group, query tile) of item it0; tile t starts at row t0 + 128 t
+  const int hl0 = tiles > 0 ? it0 / tiles : 0, tl0 = it0 - hl0 * tiles;
+  const int t0 = wq.end - 128 * tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one();
+    if (n_it > 0) {
+      int armed[C::KV_SLOTS];
+      for (int s = 0; s < C::KV_SLOTS; ++s) armed[s] = -1;
+      if (leader) {
+        mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+        tma_load_5d(smem_u32(smem), &mapK, kv_full, 0, kb, 0, kvh, bidx);
+        tma_load_5d(smem_u32(smem + C::TILE), &mapV, kv_full, 0, kb, 0, kvh, bidx);
+      }
+      int hl = hl0, tl = tl0;
+      for (int t = 0; t < n_it; ++t) {
+        const int s = t % C::KV_SLOTS;
+        const uint32_t phase = static_cast<uint32_t>((t / C::KV_SLOTS) & 1);
+        if (!mbar_wait_warp(ring_empty0 + 8 * s, phase ^ 1u, abort_flag, p.err, kSiteAttnProducer))
+          break;
+        armed[s] = static_cast<int>(phase);
+        if (leader) {
+          const uint32_t dst = smem_u32(smem + C::KV_OFF_RING + s * 2 * C::TILE);
+          mbar_arrive_expect_tx(ring_full0 + 8 * s, 2 * C::TILE);
+          tma_load_5d(dst, &mapQ, ring_full0 + 8 * s, 0, t0 + 128 * tl, 0, kvh * p.g + hl, bidx);
+          tma_load_5d(dst + C::TILE, &mapDO, ring_full0 + 8 * s, 0, t0 + 128 * tl, 0,
+                      kvh * p.g + hl, bidx);
+        }
+        __syncwarp();
+        if (++tl == tiles) {
+          tl = 0;
+          ++hl;
+        }
+      }
+      mbar_wait_drain(kv_full, 0, p.err);
+      for (int s = 0; s < C::KV_SLOTS; ++s)
+        if (armed[s] >= 0)
+          mbar_wait_drain(ring_full0 + 8 * s, static_cast<uint32_t>(armed[s]), p.err);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- UMMA issue
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = idesc16<T>(128, 128, false, false);
+    constexpr uint32_t idesc_o = idesc16<T>(128, D, false, true);
+    const uint32_t k_lo = sdesc_lo(smem_u32(smem), 16);
+    const uint32_t v_lo = sdesc_lo(smem_u32(smem + C::TILE), 16);
+    auto commit = [&](uint32_t bar) {
+      if (leader) umma_commit(bar);
+      __syncwarp();
+    };
+    auto slot_of = [&](int t) {
+      return smem_u32(smem + C::KV_OFF_RING + (t % C::KV_SLOTS) * 2 * C::TILE);
+    };
+    auto issue_s = [&](int t) -> bool {
+      if (!mbar_wait_warp(ring_full0 + 8 * (t % C::KV_SLOTS),
+                          static_cast<uint32_t>((t / C::KV_SLOTS) & 1), abort_flag, p.err,
+                          kSiteAttnMma))
+        return false;
+      tc_fence_after();
+      if (leader) bwd_issue_ss<D>(tmem + C::TM_S, k_lo, sdesc_lo(slot_of(t), 16), idesc_s);
+      __syncwarp();
+      commit(s_full);
+      return true;
+    };
+    auto issue_dp = [&](int t) {
+      if (leader)
+        bwd_issue_ss<D>(tmem + C::TM_DP, v_lo, sdesc_lo(slot_of(t) + C::TILE, 16), idesc_s);
+      __syncwarp();
+      commit(dp_full);
+    };
+    auto issue_grad = [&](int t, uint32_t bar0, uint32_t acc, uint32_t a_tm, uint32_t b_lo) {
+      for (int hh = 0; hh < 2; ++hh) {
+        if (!mbar_wait_warp(bar0 + 8 * hh, static_cast<uint32_t>(t & 1), abort_flag, p.err,
+                            kSiteAttnMma))
+          return false;
+        tc_fence_after();
+        if (leader) win_issue_ts_half<D>(acc, a_tm, b_lo, idesc_o, hh, t == 0);
+        __syncwarp();
+      }
+      return true;
+    };
+    bool ok = n_it > 0 && mbar_wait_warp(kv_full, 0, abort_flag, p.err, kSiteAttnMma) && issue_s(0);
+    if (ok) issue_dp(0);
+    for (int t = 0; t < n_it && ok; ++t) {
+      const uint32_t sl = slot_of(t);
+      // dV += P^T dO_t; then S^T_t has been read in full: the next scores go there
+      if (!(ok = issue_grad(t, p_half0, tmem + C::TM_DV, tmem + C::TM_S,
+                            sdesc_lo(sl + C::TILE, C::CHUNK))))
+        break;
+      if (t + 1 < n_it && !(ok = issue_s(t + 1))) break;
+      // dK += dS^T Q_t
+      if (!(ok = issue_grad(t, ds_half0, tmem + C::TM_DK, tmem + C::TM_DP, sdesc_lo(sl, C::CHUNK))))
+        break;
+      commit(ring_empty0 + 8 * (t % C::KV_SLOTS));
+      if (t + 1 < n_it) issue_dp(t + 1);
+    }
+    commit(acc_done);
+    commit(drain);
+    mbar_wait_drain(drain, 0, p.err);
+  } else if (warp >= 4) {
+    // --------------------------------------------------------- elementwise
+    const int e = warp & 3, half = (warp - 4) >> 2, tt = threadIdx.x - 128;
+    const int kr = e * 32 + lane, key = kb + kr;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
+    const float c = p.scale * kLog2e;
+    const float sigma = grad_sigma(p.amax);
+    const float sig = sigma * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
+    float* terms_sh = reinterpret_cast<float*>(smem + C::KV_OFF_TERMS);  // [2][a: 128, nd: 128]
+    int hl = hl0, tl = tl0;
+    auto load_terms = [&]() {
+      const int i = t0 + 128 * tl + tt;
+      return i >= 0 ? __ldg(p.terms + (static_cast<long long>(bidx) * p.h + kvh * p.g + hl) * p.nq + i)
+                    : make_float2(-INFINITY, 0.f);
+    };
+    float2 next = make_float2(-INFINITY, 0.f);
+    if (n_it > 0 && tt < 128) next = load_terms();
+    // After a wait that ran out the loop goes on, without work, so that all
+    // eight warps meet at every barrier.
+    bool ok = n_it > 0;
+    for (int t = 0; t < n_it; ++t) {
+      float* st = terms_sh + (t & 1) * 256;
+      if (tt < 128) {
+        st[tt] = next.x;
+        st[128 + tt] = next.y * sig;
+      }
+      elementwise_sync();  // (everyone is past tile t - 1, so past reading this buffer)
+      const int pq = off + t0 + 128 * tl;  // position of the tile's first query
+      if (++tl == tiles) {
+        tl = 0;
+        ++hl;
+      }
+      if (tt < 128 && t + 1 < n_it) next = load_terms();
+      const uint32_t ph = static_cast<uint32_t>(t & 1);
+      if (ok) ok = mbar_wait_warp(s_full, ph, abort_flag, p.err, kSiteAttnSoftmax);
+      tc_fence_after();
+      // every key of the block is seen by every query of the tile
+      const bool full = pq >= kb + 127 && (pq + 127 < kb + p.window || kb + 128 <= p.sinks);
+      const int q_lo = key - pq, q_hi = key < p.sinks ? 128 : key + p.window - pq;
+      uint32_t pp[32], vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (ok) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int cc = 2 * half + u;
+          uint32_t sr[32];
+          tmem_ld_32x32b_x32(t_lane + C::TM_S + cc * 32, sr);
+          tmem_ld_wait();
+          auto term = [&](int k) { return *reinterpret_cast<const float2*>(st + cc * 32 + k); };
+          if (full) {
+            if (u == 0)
+              win_p32<T, kWinBwdPolyGroups>(sr, pp, c, term, 0, 0u, false);
+            else
+              win_p32<T, kWinBwdPolyGroups>(sr, pp + 16, c, term, 1, 0u, false);
+          } else {
+            vis[u] = bits_range(q_lo, q_hi, cc);
+            win_p32<T, 0u>(sr, pp + 16 * u, c, term, u, vis[u], true);
+          }
+          tmem_st16(t_lane + C::TM_S + packed_col(cc), pp + 16 * u);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_half0 + 8 * half);
+        ok = mbar_wait_warp(dp_full, ph, abort_flag, p.err, kSiteAttnSoftmax);
+      }
+      tc_fence_after();
+      if (ok) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int cc = 2 * half + u;
+          uint32_t dr[32], ds[16];
+          tmem_ld_32x32b_x32(t_lane + C::TM_DP + cc * 32, dr);
+          tmem_ld_wait();
+          auto nd = [&](int k) { return *reinterpret_cast<const float2*>(st + 128 + cc * 32 + k); };
+          if (full)
+            win_ds32<T, false>(dr, pp + 16 * u, ds, sig, nd, 0u);
+          else
+            win_ds32<T, true>(dr, pp + 16 * u, ds, sig, nd, vis[u]);
+          tmem_st16(t_lane + C::TM_DP + packed_col(cc), ds);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_half0 + 8 * half);
+      }
+    }
+    const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
+    tc_fence_after();
+    // half 0 stores dV, half 1 dK
+    const float f = half == 0 ? exp2f(-WinScale<T>::kP) : p.scale / (sigma * WinScale<T>::kDS);
+    const uint32_t acc = t_lane + (half == 0 ? C::TM_DV : C::TM_DK);
+    if (slot0 >= 0) {
+      if (done) {  // (a part without items writes nothing and is not read)
+        float* dst = p.part + ((static_cast<long long>(bk) * p.split_parts + slot0 + part) * 2 + half) *
+                                  (128 * D) + kr * D;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(acc + cc * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(dst + cc * 32 + k) =
+                make_float4(__uint_as_float(v[k]) * f, __uint_as_float(v[k + 1]) * f,
+                            __uint_as_float(v[k + 2]) * f, __uint_as_float(v[k + 3]) * f);
+        }
+      }
+    } else {
+      T* dst = half == 0
+                   ? static_cast<T*>(p.dv) + bidx * p.dv_b + key * p.dv_n + kvh * p.dv_h
+                   : static_cast<T*>(p.dk) + bidx * p.dk_b + key * p.dk_n + kvh * p.dk_h;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t v[32];
+        if (done) {
+          tmem_ld_32x32b_x32(acc + cc * 32, v);
+          tmem_ld_wait();
+        }
+        if (key >= p.nkv) continue;
+        const bool zero = !done || key >= len;  // no query sees the key
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+          *reinterpret_cast<uint4*>(dst + cc * 32 + k) =
+              zero ? make_uint4(0u, 0u, 0u, 0u) : win_pack8<T>(v + k, f);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// Grid (cut blocks, B * hkv, 8): 32 rows of dV or dK of one block each, the
+// parts added in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) window_join_kernel(const WindowBwdParams p) {
+  const int bk = blockIdx.y, bidx = bk / p.hkv, kvh = bk - bidx * p.hkv;
+  const int which = blockIdx.z & 1, quarter = blockIdx.z >> 1;
+  int len = p.lens != nullptr ? __ldg(p.lens + bidx) : p.nkv;
+  len = min(max(len, 0), p.nkv);
+  // the blockIdx.x-th cut block and its first slot
+  int blk = 0, slot = 0, seen = 0;
+  for (;; ++blk) {
+    const int n = window_parts(p.nq, p.nkv, p.window, p.sinks, p.g, blk * 128, p.part_len);
+    if (n <= 1) continue;
+    if (seen == static_cast<int>(blockIdx.x)) break;
+    ++seen;
+    slot += n;
+  }
+  const int items = p.g * window_queries(p.nq, p.nkv, p.window, p.sinks, blk * 128,
+                                         len - (p.nkv - p.nq)).tiles();
+  const int parts = (items + p.part_len - 1) / p.part_len;  // those that have items
+  const float* src = p.part + (static_cast<long long>(bk) * p.split_parts + slot) * (2 * 128 * D) +
+                     which * (128 * D);
+  for (int x = threadIdx.x; x < 32 * D / 8; x += 256) {
+    const int kr = quarter * 32 + x / (D / 8), col = x % (D / 8) * 8, key = blk * 128 + kr;
+    if (key >= p.nkv) continue;
+    float a[8] = {};
+    if (key < len)
+      for (int q = 0; q < parts; ++q) {
+        const float4* s = reinterpret_cast<const float4*>(src + static_cast<long long>(q) * (2 * 128 * D) +
+                                                          kr * D + col);
+        const float4 u = s[0], v = s[1];
+        a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+        a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+      }
+    T* dst = which == 0 ? static_cast<T*>(p.dv) + bidx * p.dv_b + key * p.dv_n + kvh * p.dv_h
+                        : static_cast<T*>(p.dk) + bidx * p.dk_b + key * p.dk_n + kvh * p.dk_h;
+    *reinterpret_cast<uint4*>(dst + col) =
+        make_uint4(pack16<T>(a[0], a[1]), pack16<T>(a[2], a[3]), pack16<T>(a[4], a[5]),
+                   pack16<T>(a[6], a[7]));
+  }
+}
+
+// ---------------------------------------------------------------------- dQ --
+// Grid (query blocks, heads, B); the blocks with most keys first.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWinBwdThreads, 1)
+    window_dq_tc_kernel(const __grid_constant__ CUtensorMap mapQ,
+                        const __grid_constant__ CUtensorMap mapK,
+                        const __grid_constant__ CUtensorMap mapV,
+                        const __grid_constant__ CUtensorMap mapDO, const WindowBwdParams p) {
+  using C = WindowBwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::Q_OFF_BAR);
+  const uint32_t q_full = smem_u32(bars + 0);
+  const uint32_t k_full0 = smem_u32(bars + 1);   // [3]
+  const uint32_t k_empty0 = smem_u32(bars + 4);  // [3]
+  const uint32_t v_full0 = smem_u32(bars + 7);   // [2]
+  const uint32_t v_empty0 = smem_u32(bars + 9);  // [2]
+  const uint32_t s_full0 = smem_u32(bars + 11);  // [2]: S_j landed in buffer j % 2
+  const uint32_t s_free0 = smem_u32(bars + 13);  // [2]: buffer j % 2 read by every warp
+  const uint32_t dp_full = smem_u32(bars + 15);
+  const uint32_t ds_half0 = smem_u32(bars + 16);  // [2]
+  const uint32_t acc_done = smem_u32(bars + 18);
+  const uint32_t drain = smem_u32(bars + 19);
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qb = p.nqb - 1 - static_cast<int>(blockIdx.x), head = blockIdx.y, bidx = blockIdx.z;
+  const int kvh = head / p.g, off = p.nkv - p.nq;
+  int len = p.lens != nullptr ? __ldg(p.lens + bidx) : p.nkv;
+  len = min(max(len, 0), p.nkv);
+  const int p0 = off + qb * 128;
+  const int hi = min(off + min(p.nq, qb * 128 + 128), len);
+  const bool any = hi > p0;
+  const WindowKeys kt = window_keys(max(0, p0 - p.window + 1), hi, p.sinks, any);
+  const int n_kv = kt.n_s + kt.n_w;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::QK_SLOTS; ++s) {
+      mbar_init(k_full0 + 8 * s, 1);
+      mbar_init(k_empty0 + 8 * s, 1);
+    }
+    for (int s = 0; s < C::QV_SLOTS; ++s) {
+      mbar_init(v_full0 + 8 * s, 1);
+      mbar_init(v_empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full0 + 8 * b, 1);
+      mbar_init(s_free0 + 8 * b, 8);
+      mbar_init(ds_half0 + 8 * b, 4);
+    }
+    mbar_init(dp_full, 1);
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&tmem_base_sh), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort_flag = &abort_sh;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one();
+    if (n_kv > 0) {
+      int k_armed[C::QK_SLOTS], v_armed[C::QV_SLOTS];
+      for (int s = 0; s < C::QK_SLOTS; ++s) k_armed[s] = -1;
+      for (int s = 0; s < C::QV_SLOTS; ++s) v_armed[s] = -1;
+      if (leader) {
+        mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+        tma_load_5d(smem_u32(smem), &mapQ, q_full, 0, qb * 128, 0, head, bidx);
+        tma_load_5d(smem_u32(smem + C::TILE), &mapDO, q_full, 0, qb * 128, 0, head, bidx);
+      }
+      for (int j = 0; j < n_kv; ++j) {
+        const int ks = j % C::QK_SLOTS, vs = j % C::QV_SLOTS;
+        const uint32_t kph = static_cast<uint32_t>((j / C::QK_SLOTS) & 1);
+        const uint32_t vph = static_cast<uint32_t>((j / C::QV_SLOTS) & 1);
+        const int key = kt.key(j);
+        if (!mbar_wait_warp(k_empty0 + 8 * ks, kph ^ 1u, abort_flag, p.err, kSiteAttnProducer))
+          break;
+        k_armed[ks] = static_cast<int>(kph);
+        if (leader) {
+          mbar_arrive_expect_tx(k_full0 + 8 * ks, C::TILE);
+          tma_load_5d(smem_u32(smem + C::Q_OFF_K + ks * C::TILE), &mapK, k_full0 + 8 * ks, 0, key, 0,
+                      kvh, bidx);
+        }
+        __syncwarp();
+        if (!mbar_wait_warp(v_empty0 + 8 * vs, vph ^ 1u, abort_flag, p.err, kSiteAttnProducer))
+          break;
+        v_armed[vs] = static_cast<int>(vph);
+        if (leader) {
+          mbar_arrive_expect_tx(v_full0 + 8 * vs, C::TILE);
+          tma_load_5d(smem_u32(smem + C::Q_OFF_V + vs * C::TILE), &mapV, v_full0 + 8 * vs, 0, key, 0,
+                      kvh, bidx);
+        }
+        __syncwarp();
+      }
+      mbar_wait_drain(q_full, 0, p.err);
+      for (int s = 0; s < C::QK_SLOTS; ++s)
+        if (k_armed[s] >= 0)
+          mbar_wait_drain(k_full0 + 8 * s, static_cast<uint32_t>(k_armed[s]), p.err);
+      for (int s = 0; s < C::QV_SLOTS; ++s)
+        if (v_armed[s] >= 0)
+          mbar_wait_drain(v_full0 + 8 * s, static_cast<uint32_t>(v_armed[s]), p.err);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- UMMA issue
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = idesc16<T>(128, 128, false, false);
+    constexpr uint32_t idesc_o = idesc16<T>(128, D, false, true);
+    const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
+    const uint32_t do_lo = sdesc_lo(smem_u32(smem + C::TILE), 16);
+    auto commit = [&](uint32_t bar) {
+      if (leader) umma_commit(bar);
+      __syncwarp();
+    };
+    auto k_slot = [&](int j) { return smem_u32(smem + C::Q_OFF_K + (j % C::QK_SLOTS) * C::TILE); };
+    auto v_slot = [&](int j) { return smem_u32(smem + C::Q_OFF_V + (j % C::QV_SLOTS) * C::TILE); };
+    auto issue_s = [&](int j) -> bool {
+      if (!mbar_wait_warp(k_full0 + 8 * (j % C::QK_SLOTS),
+                          static_cast<uint32_t>((j / C::QK_SLOTS) & 1), abort_flag, p.err,
+                          kSiteAttnMma))
+        return false;
+      tc_fence_after();
+      if (leader)
+        bwd_issue_ss<D>(tmem + C::TQ_S + 128u * static_cast<uint32_t>(j & 1), q_lo,
+                        sdesc_lo(k_slot(j), 16), idesc_s);
+      __syncwarp();
+      commit(s_full0 + 8 * (j & 1));
+      return true;
+    };
+    auto issue_dp = [&](int j) -> bool {
+      if (!mbar_wait_warp(v_full0 + 8 * (j % C::QV_SLOTS),
+                          static_cast<uint32_t>((j / C::QV_SLOTS) & 1), abort_flag, p.err,
+                          kSiteAttnMma))
+        return false;
+      tc_fence_after();
+      if (leader) bwd_issue_ss<D>(tmem + C::TQ_DP, do_lo, sdesc_lo(v_slot(j), 16), idesc_s);
+      __syncwarp();
+      commit(dp_full);
+      commit(v_empty0 + 8 * (j % C::QV_SLOTS));
+      return true;
+    };
+    bool ok = n_kv > 0 && mbar_wait_warp(q_full, 0, abort_flag, p.err, kSiteAttnMma) &&
+              issue_s(0) && issue_dp(0) && (n_kv < 2 || issue_s(1));
+    for (int j = 0; j < n_kv && ok; ++j) {
+      for (int hh = 0; hh < 2; ++hh) {
+        if (!mbar_wait_warp(ds_half0 + 8 * hh, static_cast<uint32_t>(j & 1), abort_flag, p.err,
+                            kSiteAttnMma)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (leader)
+          win_issue_ts_half<D>(tmem + C::TQ_A, tmem + C::TQ_DP, sdesc_lo(k_slot(j), C::CHUNK),
+                               idesc_o, hh, j == 0);
+        __syncwarp();
+      }
+      if (!ok) break;
+      commit(k_empty0 + 8 * (j % C::QK_SLOTS));
+      // dP_j+1 overwrites dS_j: after dQ_j (in order) and after every warp's
+      // hand-over of dS_j (all of dP_j has been read)
+      if (j + 1 < n_kv && !(ok = issue_dp(j + 1))) break;
+      if (j + 2 < n_kv) {
+        if (!mbar_wait_warp(s_free0 + 8 * (j & 1), static_cast<uint32_t>((j >> 1) & 1), abort_flag,
+                            p.err, kSiteAttnMma) ||
+            !issue_s(j + 2)) {
+          ok = false;
+          break;
+        }
+      }
+    }
+    commit(acc_done);
+    commit(drain);
+    mbar_wait_drain(drain, 0, p.err);
+  } else if (warp >= 4) {
+    // --------------------------------------------------------- elementwise
+    const int e = warp & 3, half = (warp - 4) >> 2;
+    const int qr = e * 32 + lane, i = qb * 128 + qr, pos = p0 + qr;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
+    const float c = p.scale * kLog2e;
+    const float sigma = grad_sigma(p.amax);
+    const float sig = sigma * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
+    float2 tr = make_float2(-INFINITY, 0.f);
+    if (i < p.nq) tr = __ldg(p.terms + (static_cast<long long>(bidx) * p.h + head) * p.nq + i);
+    const float2 a2 = make_float2(tr.x, tr.x), nd2 = make_float2(tr.y * sig, tr.y * sig);
+    auto term = [&](int) { return a2; };
+    auto nd = [&](int) { return nd2; };
+    bool ok = n_kv > 0;
+    for (int j = 0; j < n_kv && ok; ++j) {
+      if (!mbar_wait_warp(s_full0 + 8 * (j & 1), static_cast<uint32_t>((j >> 1) & 1), abort_flag,
+                          p.err, kSiteAttnSoftmax)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int kb = kt.key(j);
+      const bool sink = j < kt.n_s;
+      const bool full = !sink && kb + 127 <= p0 && kb >= kt.lo && kb >= p0 + 128 - p.window;
+      const uint32_t tS = t_lane + C::TQ_S + 128u * static_cast<uint32_t>(j & 1);
+      uint32_t pp[32], vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int cc = 2 * half + u;
+        uint32_t sr[32];
+        tmem_ld_32x32b_x32(tS + cc * 32, sr);
+        tmem_ld_wait();
+        if (u == 1) {
+          // this warp's scores of buffer j % 2 are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free0 + 8 * (j & 1));
+        }
+        if (full) {
+          if (u == 0)
+            win_p32<T, kWinBwdPolyGroups>(sr, pp, c, term, 0, 0u, false);
+          else
+            win_p32<T, kWinBwdPolyGroups>(sr, pp + 16, c, term, 1, 0u, false);
+        } else {
+          vis[u] = sink ? bits_range(0, kt.ns - kb, cc)
+                        : window_bits(pos, kb, kt.lo, p.window, p.sinks, cc);
+          win_p32<T, 0u>(sr, pp + 16 * u, c, term, u, vis[u], true);
+        }
+      }
+      if (!mbar_wait_warp(dp_full, static_cast<uint32_t>(j & 1), abort_flag, p.err,
+                          kSiteAttnSoftmax)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int cc = 2 * half + u;
+        uint32_t dr[32], ds[16];
+        tmem_ld_32x32b_x32(t_lane + C::TQ_DP + cc * 32, dr);
+        tmem_ld_wait();
+        if (full)
+          win_ds32<T, false>(dr, pp + 16 * u, ds, sig, nd, 0u);
+        else
+          win_ds32<T, true>(dr, pp + 16 * u, ds, sig, nd, vis[u]);
+        tmem_st16(t_lane + C::TQ_DP + packed_col(cc), ds);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_half0 + 8 * half);
+    }
+    const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
+    tc_fence_after();
+    const float f = p.scale / (sigma * WinScale<T>::kDS);
+    T* dst = static_cast<T*>(p.dq) + bidx * p.dq_b + i * p.dq_n + head * p.dq_h;
+    // each half stores its half of the columns
+#pragma unroll 1
+    for (int cc = half * (D / 64); cc < (half + 1) * (D / 64); ++cc) {
+      uint32_t v[32];
+      if (done) {
+        tmem_ld_32x32b_x32(t_lane + C::TQ_A + cc * 32, v);
+        tmem_ld_wait();
+      }
+      if (i >= p.nq) continue;
+      const bool zero = !done || pos >= len;
+#pragma unroll
+      for (int k = 0; k < 32; k += 8)
+        *reinterpret_cast<uint4*>(dst + cc * 32 + k) =
+            zero ? make_uint4(0u, 0u, 0u, 0u) : win_pack8<T>(v + k, f);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace bpt

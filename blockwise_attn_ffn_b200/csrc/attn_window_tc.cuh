@@ -36,6 +36,7 @@
 
 #include <type_traits>
 
+#include "attn_pair_tc.cuh"
 #include "cache.cuh"
 #include "common.cuh"
 
@@ -131,6 +132,25 @@ __device__ __forceinline__ WindowTile window_tile(const WindowParams& p, int qb,
   return t;
 }
 
+// The 128-key tiles over which queries whose windows start at `lo` at the
+// earliest and whose last visible key is hi - 1 run: sink tiles from key 0,
+// then window tiles that end at hi.  Where the two would overlap, window tiles
+// from key 0 serve both (so a sink tile never reaches past hi).
+struct WindowKeys {
+  int lo, ns, n_s, n_w, w0;  // window keys from lo, sinks before it, tiles, first window tile's key
+  __device__ __forceinline__ int key(int j) const { return j < n_s ? 128 * j : w0 + 128 * (j - n_s); }
+};
+__device__ __forceinline__ WindowKeys window_keys(int lo, int hi, int sinks, bool any) {
+  WindowKeys k;
+  k.lo = lo;
+  k.ns = min(sinks, lo);
+  k.n_s = any ? (k.ns + 127) / 128 : 0;
+  if (lo < 128 * k.n_s) k.lo = k.ns = k.n_s = 0;
+  k.n_w = any ? (hi - k.lo + 127) / 128 : 0;
+  k.w0 = hi - 128 * k.n_w;
+  return k;
+}
+
 // The visible bits of keys kb + 32 w .. of a window tile for the row at p:
 // keys lo .. p that are within the window or sinks.
 __device__ __forceinline__ uint32_t window_bits(int p, int kb, int lo, int window, int sinks,
@@ -179,29 +199,6 @@ __device__ __noinline__ void window_row_slow(const WindowParams& p, int b, int h
   for (int c = 0; c < D / 32; ++c) dst[lane + 32 * c] = static_cast<T>(o[c] / l);
 }
 
-__device__ __forceinline__ void window_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void window_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void window_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                   taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-               "r"(r[7])
-               : "memory");
-}
-
 // 16-column groups (of eight per row) whose exp2 runs as a cubic on the FMA
 // pipe, so that it shares the work of the exponential unit (unmasked tiles).
 constexpr uint32_t kWindowPolyGroups = 0x88u;
@@ -241,12 +238,8 @@ __global__ void __launch_bounds__(384, 1)
   const WindowTile tA = window_tile(p, qbA, len), tB = window_tile(p, qbB, len);
   const bool anyA = tA.any(), anyB = has_b && tB.any();
   // (block A is never after block B: if A has no valid row, B has none)
-  const int lo = tA.lo, hi = anyB ? tB.hi : tA.hi;
-  const int ns = min(p.sinks, lo);
-  const int n_s = anyA ? (ns + 127) / 128 : 0;
-  const int n_w = anyA ? (hi - lo + 127) / 128 : 0;
-  const int n_kv = n_s + n_w;
-  const int w0 = hi - 128 * n_w;  // first key of the window tiles
+  const WindowKeys kt = window_keys(tA.lo, anyB ? tB.hi : tA.hi, p.sinks, anyA);
+  const int lo = kt.lo, ns = kt.ns, n_s = kt.n_s, w0 = kt.w0, n_kv = kt.n_s + kt.n_w;
   // tiles seen by a query tile: the sink tiles and first .. last (sinks past
   // lo lie in the window tiles, so there a tile starts at lo too)
   auto first_of = [&](const WindowTile& t) {
@@ -259,7 +252,6 @@ __global__ void __launch_bounds__(384, 1)
     if (x == 0) return anyA && (j < n_s || (j >= fA && j <= lA));
     return anyB && (j < n_s || (j >= fB && j <= lB));
   };
-  auto key_of = [&](int j) { return j < n_s ? 128 * j : w0 + 128 * (j - n_s); };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -301,7 +293,7 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int j = 0; j < n_kv && ok; ++j) {
-        const int kb = key_of(j);
+        const int kb = kt.key(j);
         for (int w = 0; w < 2; ++w) {
           if (!mbar_wait_warp(ring_empty0 + 8 * slot, phase ^ 1u, abort_flag, p.err,
                               kSiteAttnProducer)) {
@@ -452,7 +444,7 @@ __global__ void __launch_bounds__(384, 1)
       for (int cc = 0; cc < 4; ++cc)
         tmem_ld_32x32b_x32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
       tmem_ld_wait();
-      const int kb = key_of(j);
+      const int kb = kt.key(j);
       // a window tile that every row of the block sees whole
       const bool full = j >= n_s && kb + 127 <= p0 && kb >= lo && kb >= p0 + 128 - p.window;
       if (!full) {
@@ -490,11 +482,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
         for (int cc = 0; cc < D / 8; ++cc) {
           uint32_t v[8];
-          window_ld8(tO + cc * 8, v);
+          tmem_ld_32x32b_x8(tO + cc * 8, v);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-          window_st8(tO + cc * 8, v);
+          tmem_st_32x32b_x8(tO + cc * 8, v);
         }
       }
       // a row that has seen no key yet keeps reference 0: exp2(-inf) = 0
@@ -520,7 +512,7 @@ __global__ void __launch_bounds__(384, 1)
             sum2[(k >> 1) & 3] = __fadd2_rn(sum2[(k >> 1) & 3], e2);
             pk[k >> 1] = pack16<T>(e2.x, e2.y);
           }
-          window_st16(tS + cc * 16, pk);
+          tmem_st_32x32b_x16(tS + cc * 16, pk);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();

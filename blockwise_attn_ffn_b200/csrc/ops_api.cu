@@ -21,6 +21,7 @@
 // the namespace gets its own name, so that both units link into one library.
 #define bpt bpt_ops
 #include "attn_decode.cuh"
+#include "attn_window_bwd_tc.cuh"
 #include "attn_window_tc.cuh"
 #include "cache.cuh"
 #include "common.cuh"
@@ -88,7 +89,15 @@ bpt_status ops_device(int* sms) {
          smem_fails(bpt::attn_window_tc_kernel<bf, 64>, bpt::WindowCfg<64>::SMEM) ||
          smem_fails(bpt::attn_window_tc_kernel<bf, 128>, bpt::WindowCfg<128>::SMEM) ||
          smem_fails(bpt::attn_window_tc_kernel<__half, 64>, bpt::WindowCfg<64>::SMEM) ||
-         smem_fails(bpt::attn_window_tc_kernel<__half, 128>, bpt::WindowCfg<128>::SMEM)))
+         smem_fails(bpt::attn_window_tc_kernel<__half, 128>, bpt::WindowCfg<128>::SMEM) ||
+         smem_fails(bpt::window_dkv_tc_kernel<bf, 64>, bpt::WindowBwdCfg<64>::KV_SMEM) ||
+         smem_fails(bpt::window_dkv_tc_kernel<bf, 128>, bpt::WindowBwdCfg<128>::KV_SMEM) ||
+         smem_fails(bpt::window_dkv_tc_kernel<__half, 64>, bpt::WindowBwdCfg<64>::KV_SMEM) ||
+         smem_fails(bpt::window_dkv_tc_kernel<__half, 128>, bpt::WindowBwdCfg<128>::KV_SMEM) ||
+         smem_fails(bpt::window_dq_tc_kernel<bf, 64>, bpt::WindowBwdCfg<64>::Q_SMEM) ||
+         smem_fails(bpt::window_dq_tc_kernel<bf, 128>, bpt::WindowBwdCfg<128>::Q_SMEM) ||
+         smem_fails(bpt::window_dq_tc_kernel<__half, 64>, bpt::WindowBwdCfg<64>::Q_SMEM) ||
+         smem_fails(bpt::window_dq_tc_kernel<__half, 128>, bpt::WindowBwdCfg<128>::Q_SMEM)))
       return BPT_ERR_CUDA;
     d.init = true;
   }
@@ -236,8 +245,8 @@ bpt_status check_window(const bpt_window* w) {
       w->sinks < 0)
     return BPT_ERR_INVALID_ARG;
   if (w->d_k != 64 && w->d_k != 128) return BPT_ERR_UNSUPPORTED;
-  const int64_t lim = int64_t(1) << 30;
-  if (w->n_kv > lim || w->heads > lim || w->batch > lim) return BPT_ERR_UNSUPPORTED;
+  const int64_t lim = int64_t(1) << 30;  // (key + window stays below 2^31)
+  if (w->n_kv > lim / 2 || w->heads > lim || w->batch > lim) return BPT_ERR_UNSUPPORTED;
   // CTAs of a launch (a 31-bit grid), one per two query tiles at most
   const int64_t tiles = (w->n_kv + 127) / 128, hb = w->heads * std::max<int64_t>(1, w->batch);
   if (hb >= lim || tiles >= (int64_t(1) << 31) / hb) return BPT_ERR_UNSUPPORTED;
@@ -278,6 +287,73 @@ cudaError_t launch_window(const CUtensorMap& q, const CUtensorMap& k, const CUte
   using C = bpt::WindowCfg<D>;
   bpt::attn_window_tc_kernel<T, D>
       <<<unsigned(batch * p.hkv * p.npairs), C::THREADS, C::SMEM, s>>>(q, k, v, p);
+  return cudaGetLastError();
+}
+
+// Parts of the dK/dV work and workspace of the backward.
+struct WindowBwdPlan {
+  int part_len;
+  int64_t parts, cut_parts, cut_blocks;  // per (sequence, kv head)
+  size_t off_terms, off_part, total;
+};
+constexpr int kPlanSms = 148;  // the GPU the work is cut for
+constexpr size_t kAmaxOffset = 64;
+
+WindowBwdPlan window_bwd_plan(const bpt_window* w) {
+  WindowBwdPlan p{};
+  const int nq = int(w->n_q), nkv = int(w->n_kv), g = int(w->heads / w->kv_heads);
+  const int win = int(std::min<int64_t>(w->window, nkv)), snk = int(std::min<int64_t>(w->sinks, nkv));
+  const int nblk = (nkv + 127) / 128;
+  int64_t items = 0;
+  for (int b = 0; b < nblk; ++b)
+    items += int64_t(g) * bpt::window_queries(nq, nkv, win, snk, b * 128, nq).tiles();
+  items *= w->batch * w->kv_heads;
+  // half of one SM's share, at least 8 items (a part costs 128 KB of traffic
+  // and a join, about what an item costs)
+  p.part_len = int(std::min<int64_t>(0x7FFFFFFF, std::max<int64_t>(
+      8, (items + 2 * kPlanSms - 1) / (2 * kPlanSms))));
+  for (int b = 0; b < nblk; ++b) {
+    const int n = bpt::window_parts(nq, nkv, win, snk, g, b * 128, p.part_len);
+    p.parts += n;
+    if (n > 1) {
+      p.cut_parts += n;
+      p.cut_blocks += 1;
+    }
+  }
+  p.off_terms = kOpsHeader;
+  p.off_part = align_to(p.off_terms + size_t(w->batch * w->heads) * size_t(w->n_q) * 8, 256);
+  p.total = align_to(p.off_part + size_t(w->batch * w->kv_heads) * size_t(p.cut_parts) *
+                                      size_t(2 * 128 * 4) * size_t(w->d_k), 256);
+  return p;
+}
+
+bpt_status check_window_bwd(const bpt_window* w) {
+  const bpt_status st = check_window(w);
+  if (st != BPT_OK) return st;
+  if (w->batch > 65535 || w->heads > 65535 || w->batch * w->kv_heads > 65535 ||
+      w->n_q >= (int64_t(1) << 34) / std::max<int64_t>(1, w->batch * w->heads))
+    return BPT_ERR_UNSUPPORTED;
+  return BPT_OK;
+}
+
+template <typename T, int D>
+cudaError_t launch_window_bwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              const CUtensorMap& d_o, const bpt::WindowTermsParams& tp,
+                              const bpt::WindowBwdParams& p, const WindowBwdPlan& plan,
+                              int64_t batch, cudaStream_t s) {
+  using C = bpt::WindowBwdCfg<D>;
+  const int64_t rows = batch * p.nq * p.h, per = 256 / (D / 8);
+  if (rows > 0)
+    bpt::window_terms_kernel<T, D><<<unsigned((rows + per - 1) / per), 256, 0, s>>>(tp);
+  bpt::window_dkv_tc_kernel<T, D>
+      <<<dim3(unsigned(plan.parts), unsigned(batch * p.hkv)), bpt::kWinBwdThreads, C::KV_SMEM, s>>>(
+          q, k, v, d_o, p);
+  if (plan.cut_blocks > 0)
+    bpt::window_join_kernel<T, D>
+        <<<dim3(unsigned(plan.cut_blocks), unsigned(batch * p.hkv), 8), 256, 0, s>>>(p);
+  bpt::window_dq_tc_kernel<T, D>
+      <<<dim3(unsigned(p.nqb), unsigned(p.h), unsigned(batch)), bpt::kWinBwdThreads, C::Q_SMEM,
+         s>>>(q, k, v, d_o, p);
   return cudaGetLastError();
 }
 
@@ -581,6 +657,108 @@ bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const
   else
     e = dk == 128 ? launch_window<__half, 128>(mq, mk, mv, p, B, s)
                   : launch_window<__half, 64>(mq, mk, mv, p, B, s);
+  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status bpt_attn_window_backward_workspace_size(const bpt_window* w, size_t* bytes) {
+  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
+  const bpt_status st = check_window_bwd(w);
+  if (st != BPT_OK) return st;
+  *bytes = window_bwd_plan(w).total;
+  return BPT_OK;
+}
+
+bpt_status bpt_attn_window_backward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
+                                    const bpt_rows* v, const bpt_rows* o, const float* stats,
+                                    const bpt_rows* d_o, const int32_t* lens, const bpt_rows* dq,
+                                    const bpt_rows* dk, const bpt_rows* dv, void* workspace,
+                                    size_t workspace_bytes, bpt_stream_t stream) {
+  bpt_status st = check_window_bwd(w);
+  if (st != BPT_OK) return st;
+  for (const bpt_rows* r : {q, k, v, o, d_o, dq, dk, dv})
+    if (r == nullptr) return BPT_ERR_INVALID_ARG;
+  const int64_t B = w->batch, nq = w->n_q, nkv = w->n_kv, h = w->heads, hkv = w->kv_heads,
+                c = w->d_k;
+  // (with keys but without queries the gradients of the keys are zeros: the
+  // call would be of no use and is refused)
+  if (B == 0 || nkv == 0) return BPT_OK;
+  if (nq == 0) return BPT_ERR_INVALID_ARG;
+  if (!rows_ok(*q, B, nq, h) || !rows_ok(*k, B, nkv, hkv) || !rows_ok(*v, B, nkv, hkv) ||
+      !rows_ok(*o, B, nq, h) || !rows_ok(*d_o, B, nq, h) || !rows_ok(*dq, B, nq, h) ||
+      !rows_ok(*dk, B, nkv, hkv) || !rows_ok(*dv, B, nkv, hkv) ||
+      !rows_apart(*dq, B, nq, h, c) || !rows_apart(*dk, B, nkv, hkv, c) ||
+      !rows_apart(*dv, B, nkv, hkv, c) || stats == nullptr || unaligned(stats, 8) ||
+      unaligned(lens, 4) || workspace == nullptr || unaligned(workspace, 256))
+    return BPT_ERR_INVALID_ARG;
+  const WindowBwdPlan plan = window_bwd_plan(w);
+  if (workspace_bytes < plan.total) return BPT_ERR_WORKSPACE;
+  const Range rq = rows_range(*q, B, nq, h, c), rk = rows_range(*k, B, nkv, hkv, c),
+              rv = rows_range(*v, B, nkv, hkv, c), ro = rows_range(*o, B, nq, h, c),
+              rd = rows_range(*d_o, B, nq, h, c), rl(lens, size_t(B) * 4),
+              rs(stats, size_t(B * h) * size_t(nq) * 8), rw(workspace, plan.total);
+  // Gradients may interleave with one another (the parts of one packed
+  // gradient), not with what is read.
+  for (const Range& r : {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
+                         rows_range(*dv, B, nkv, hkv, c), rw})
+    if (any_meets(r, {rq, rk, rv, ro, rd, rl, rs})) return BPT_ERR_INVALID_ARG;
+  if (any_meets(rw, {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
+                     rows_range(*dv, B, nkv, hkv, c)}) ||
+      dq->data == dk->data || dq->data == dv->data || dk->data == dv->data)
+    return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  st = ops_encoder();
+  if (st != BPT_OK) return st;
+  CUtensorMap mq, mk, mv, md;
+  if (!map_rows(&mq, *q, B, nq, h, c) || !map_rows(&mk, *k, B, nkv, hkv, c) ||
+      !map_rows(&mv, *v, B, nkv, hkv, c) || !map_rows(&md, *d_o, B, nq, h, c))
+    return BPT_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* amax = nullptr;
+  if (w->dtype == BPT_F16) {
+    amax = reinterpret_cast<uint32_t*>(ws + kAmaxOffset);
+    if (cudaMemsetAsync(amax, 0, 4, s) != cudaSuccess) return BPT_ERR_CUDA;
+  }
+  bpt::WindowTermsParams tp{};
+  tp.o = o->data;
+  tp.o_b = o->stride_b; tp.o_n = o->stride_n; tp.o_h = o->stride_h;
+  tp.d_o = d_o->data;
+  tp.d_b = d_o->stride_b; tp.d_n = d_o->stride_n; tp.d_h = d_o->stride_h;
+  tp.stats = reinterpret_cast<const float2*>(stats);
+  tp.terms = reinterpret_cast<float2*>(ws + plan.off_terms);
+  tp.amax = amax;
+  tp.lens = lens;
+  tp.B = int(B); tp.nq = int(nq); tp.nkv = int(nkv); tp.h = int(h);
+  tp.err = reinterpret_cast<uint32_t*>(ws);
+  bpt::WindowBwdParams p{};
+  p.nq = int(nq); p.nkv = int(nkv); p.h = int(h); p.hkv = int(hkv); p.g = int(h / hkv);
+  p.nqb = int((nq + 127) / 128); p.nblk = int((nkv + 127) / 128);
+  p.window = int(std::min<int64_t>(w->window, nkv));
+  p.sinks = int(std::min<int64_t>(w->sinks, nkv));
+  p.lens = lens;
+  p.terms = tp.terms;
+  p.amax = amax;
+  p.dq = dq->data;
+  p.dq_b = dq->stride_b; p.dq_n = dq->stride_n; p.dq_h = dq->stride_h;
+  p.dk = dk->data;
+  p.dk_b = dk->stride_b; p.dk_n = dk->stride_n; p.dk_h = dk->stride_h;
+  p.dv = dv->data;
+  p.dv_b = dv->stride_b; p.dv_n = dv->stride_n; p.dv_h = dv->stride_h;
+  p.scale = float(1.0 / std::sqrt(double(c)));
+  p.part_len = plan.part_len;
+  p.split_parts = int(plan.cut_parts);
+  p.part = reinterpret_cast<float*>(ws + plan.off_part);
+  p.err = tp.err;
+  cudaError_t e;
+  using bf = __nv_bfloat16;
+  if (w->dtype == BPT_BF16)
+    e = c == 128 ? launch_window_bwd<bf, 128>(mq, mk, mv, md, tp, p, plan, B, s)
+                 : launch_window_bwd<bf, 64>(mq, mk, mv, md, tp, p, plan, B, s);
+  else
+    e = c == 128 ? launch_window_bwd<__half, 128>(mq, mk, mv, md, tp, p, plan, B, s)
+                 : launch_window_bwd<__half, 64>(mq, mk, mv, md, tp, p, plan, B, s);
   return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
 

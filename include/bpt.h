@@ -749,6 +749,28 @@ bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const
                                    float* stats, void* workspace, size_t workspace_bytes,
                                    bpt_stream_t stream);
 
+/*
+ * bpt_attn_window_backward -- gradients of bpt_attn_window_forward.
+ * q, k, v, lens as there; o its output, stats its (m, l); d_o the gradient of
+ * o.  dq [batch, n_q, heads, d_k] and dk, dv [batch, n_kv, kv_heads, d_k] are
+ * written whole (zeros where nothing flows: rows past the length, keys that
+ * no query sees), dk and dv summed over the query heads that share a kv head:
+ *     P = exp(s - m) / l,  dS = P (d_o V^T - rowsum(d_o o)),
+ *     dv = P^T d_o,  dk = dS^T q / sqrt(d_k),  dq = dS k / sqrt(d_k).
+ * fp32 accumulation in a fixed order: results do not depend on timing.
+ * Rows past a length are not read into any product (they may hold NaN); other
+ * values have to be finite: one that is not may turn any gradient of its
+ * sequence into NaN.  The three gradients may be the interleaved parts of one
+ * packed tensor; they may not overlap what is read.  n_q = 0 with n_kv > 0 is
+ * refused; batch, heads and batch * kv_heads are at most 65535.
+ */
+bpt_status bpt_attn_window_backward_workspace_size(const bpt_window* w, size_t* bytes);
+bpt_status bpt_attn_window_backward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
+                                    const bpt_rows* v, const bpt_rows* o, const float* stats,
+                                    const bpt_rows* d_o, const int32_t* lens, const bpt_rows* dq,
+                                    const bpt_rows* dk, const bpt_rows* dv, void* workspace,
+                                    size_t workspace_bytes, bpt_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
