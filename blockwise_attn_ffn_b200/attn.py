@@ -13,7 +13,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .cache import HEADER_BYTES, check, check_workspace, code_of, new_workspace, on_device, rows_check
+from .cache import (HEADER_BYTES, check, check_workspace, code_of, new_workspace, rows_check, run,
+                    stream_of)
 
 
 def _window(q, k, window, sinks) -> "_lib.Window":
@@ -23,10 +24,8 @@ def _window(q, k, window, sinks) -> "_lib.Window":
     return _lib.Window(B, nq, k.shape[1], h, k.shape[2], dk, window, sinks, code_of(q, "q"), 0)
 
 
-def _rows(t: torch.Tensor, what: str, shape, dtype, device) -> "_lib.Rows":
-    p = rows_check(t, what, shape, dtype, device)
-    sb, sn, sh, _ = t.stride()
-    return _lib.Rows(p, sb, sn, sh)
+def _rows(t: torch.Tensor, what: str, shape: tuple, dtype, index: int) -> "_lib.Rows":
+    return _lib.Rows(rows_check(t, what, shape, dtype, index), *t.stride()[:3])
 
 
 def attn_window_workspace(q: torch.Tensor, k: torch.Tensor, window: int,
@@ -50,19 +49,18 @@ def attn_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, windo
     w = _window(q, k, window, sinks)
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    dev, dt = q.device, q.dtype
-    qs, ks = (w.batch, w.n_q, w.heads, w.d_k), (w.batch, w.n_kv, w.kv_heads, w.d_k)
+    index, dt, qs = q.get_device(), q.dtype, q.shape
+    B, nq, h, dk = qs
+    ks = (B, k.shape[1], k.shape[2], dk)
     if out is None:
-        out = torch.empty(qs, dtype=dt, device=dev)
-    rows = (_rows(q, "q", qs, dt, dev), _rows(k, "k", ks, dt, dev), _rows(v, "v", ks, dt, dev))
-    lp = None if lens is None else check(lens, "lens", (w.batch,), torch.int32, dev)
-    sp = None if stats is None else check(stats, "stats", (w.batch, w.heads, w.n_q, 2),
-                                          torch.float32, dev)
-    ws = new_workspace(HEADER_BYTES, dev) if ws is None else check_workspace(ws, dev)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with on_device(dev):
-        st = _lib.bpt_attn_window_forward(w, *rows, lp, _rows(out, "out", qs, dt, dev), sp,
-                                          ws.data_ptr(), ws.numel(), s.cuda_stream)
+        out = torch.empty(qs, dtype=dt, device=q.device)
+    lp = None if lens is None else check(lens, "lens", (B,), torch.int32, index)
+    sp = None if stats is None else check(stats, "stats", (B, h, nq, 2), torch.float32, index)
+    ws = new_workspace(HEADER_BYTES, q.device) if ws is None else check_workspace(ws, index)
+    st = run(_lib.bpt_attn_window_forward, index, w, _rows(q, "q", qs, dt, index),
+             _rows(k, "k", ks, dt, index), _rows(v, "v", ks, dt, index), lp,
+             _rows(out, "out", qs, dt, index), sp, ws.data_ptr(), ws.numel(),
+             stream_of(stream, index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_window_forward")
     return out
@@ -88,24 +86,24 @@ def attn_window_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
     w = _window(q, k, window, sinks)
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    dev, dt = q.device, q.dtype
-    qs, ks = (w.batch, w.n_q, w.heads, w.d_k), (w.batch, w.n_kv, w.kv_heads, w.d_k)
+    index, dt, qs = q.get_device(), q.dtype, q.shape
+    B, nq, h, dk = qs
+    ks = (B, k.shape[1], k.shape[2], dk)
     if grads is None:
-        grads = (torch.empty(qs, dtype=dt, device=dev), torch.empty(ks, dtype=dt, device=dev),
-                 torch.empty(ks, dtype=dt, device=dev))
-    lp = None if lens is None else check(lens, "lens", (w.batch,), torch.int32, dev)
+        grads = (torch.empty(qs, dtype=dt, device=q.device),
+                 torch.empty(ks, dtype=dt, device=q.device),
+                 torch.empty(ks, dtype=dt, device=q.device))
+    lp = None if lens is None else check(lens, "lens", (B,), torch.int32, index)
     if ws is None:
         ws = attn_window_backward_workspace(q, k, window, sinks)
-    check_workspace(ws, dev)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with on_device(dev):
-        st = _lib.bpt_attn_window_backward(
-            w, _rows(q, "q", qs, dt, dev), _rows(k, "k", ks, dt, dev), _rows(v, "v", ks, dt, dev),
-            _rows(o, "o", qs, dt, dev),
-            check(stats, "stats", (w.batch, w.heads, w.n_q, 2), torch.float32, dev),
-            _rows(d_o, "d_o", qs, dt, dev), lp, _rows(grads[0], "dq", qs, dt, dev),
-            _rows(grads[1], "dk", ks, dt, dev), _rows(grads[2], "dv", ks, dt, dev), ws.data_ptr(),
-            ws.numel(), s.cuda_stream)
+    check_workspace(ws, index)
+    st = run(_lib.bpt_attn_window_backward, index, w, _rows(q, "q", qs, dt, index),
+             _rows(k, "k", ks, dt, index), _rows(v, "v", ks, dt, index),
+             _rows(o, "o", qs, dt, index),
+             check(stats, "stats", (B, h, nq, 2), torch.float32, index),
+             _rows(d_o, "d_o", qs, dt, index), lp, _rows(grads[0], "dq", qs, dt, index),
+             _rows(grads[1], "dk", ks, dt, index), _rows(grads[2], "dv", ks, dt, index),
+             ws.data_ptr(), ws.numel(), stream_of(stream, index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_window_backward")
     return grads

@@ -14,7 +14,6 @@ device: no call synchronises, and every call may be captured into a graph.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
@@ -33,11 +32,17 @@ def code_of(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def on_device(device: torch.device):
-    """A context in which `device` is the current one (nothing if it already is)."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def stream_of(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    """The raw stream of a call on device `index` (the current one's by default)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def run(fn, index: int, *args) -> int:
+    """fn(*args) with device `index` current."""
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def new_workspace(nbytes: int, device) -> torch.Tensor:
@@ -46,43 +51,45 @@ def new_workspace(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
-def check(t: torch.Tensor, what: str, shape, dtype, device) -> int:
-    """The address of a contiguous tensor of this shape, type and device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() \
-            or t.device != device:
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}, "
-                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+def _refuse(t: torch.Tensor, what: str, shape, dtype, index: int, how: str):
+    raise ValueError(f"{what} must be a {dtype} tensor {list(shape)} on cuda:{index}, {how}; got "
+                     f"{t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
+
+
+def check(t: torch.Tensor, what: str, shape: tuple, dtype, index: int) -> int:
+    """The address of a contiguous tensor of this shape and type on device `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index \
+            or not t.is_contiguous():
+        _refuse(t, what, shape, dtype, index, "contiguous")
     return t.data_ptr()
 
 
-def check_workspace(ws: torch.Tensor, device) -> torch.Tensor:
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+def check_workspace(ws: torch.Tensor, index: int) -> torch.Tensor:
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{index}")
     return ws
 
 
-def rows_check(t: torch.Tensor, what: str, shape, dtype, device) -> int:
+def rows_check(t: torch.Tensor, what: str, shape: tuple, dtype, index: int) -> int:
     """The address of a tensor whose last dimension is contiguous."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device \
-            or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{what} must be a {dtype} tensor {list(shape)} on {device} with its last "
-                         f"dimension contiguous, got {t.dtype} {list(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or t.stride(-1) != 1:
+        _refuse(t, what, shape, dtype, index, "its last dimension contiguous")
     return t.data_ptr()
 
 
 def _cache(k_cache, v_cache, page_table, lens) -> "_lib.Cache":
     if k_cache.dim() != 4 or not k_cache.is_cuda or not k_cache.is_contiguous():
         raise ValueError("k_cache must be a contiguous CUDA tensor [pages, kv_heads, page_size, d_k]")
-    dev = k_cache.device
+    index = k_cache.get_device()
     code = code_of(k_cache, "k_cache")
-    pages, hkv, ps, dk = k_cache.shape
+    shape = k_cache.shape
+    pages, hkv, ps, dk = shape
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, per = page_table.shape
-    return _lib.Cache(k_cache.data_ptr(),
-                      check(v_cache, "v_cache", k_cache.shape, k_cache.dtype, dev),
-                      check(page_table, "page_table", page_table.shape, torch.int32, dev),
-                      check(lens, "lens", (B,), torch.int32, dev),
+    return _lib.Cache(k_cache.data_ptr(), check(v_cache, "v_cache", shape, k_cache.dtype, index),
+                      check(page_table, "page_table", (B, per), torch.int32, index),
+                      check(lens, "lens", (B,), torch.int32, index),
                       B, pages, hkv, ps, dk, per, code, 0)
 
 
@@ -125,28 +132,24 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     multiples of 8 elements, last dimension contiguous) behind each sequence;
     returns new_lens [B] (allocated if not given; not the lens tensor)."""
     c = _cache(k_cache, v_cache, page_table, lens)
-    dev, B = k_cache.device, c.batch
+    index, dt, B = k_cache.get_device(), k_cache.dtype, lens.shape[0]
     if k.dim() != 4:
         raise ValueError("k must be [B, T, kv_heads, d_k]")
+    _, hkv, ps, dk = k_cache.shape
     T = k.shape[1]
-    shape = (B, T, c.kv_heads, c.d_k)
-    kp = rows_check(k, "k", shape, k_cache.dtype, dev)
-    vp = rows_check(v, "v", shape, k_cache.dtype, dev)
-    slots = (B, c.kv_heads, c.max_pages * c.page_size)
+    shape, slots = (B, T, hkv, dk), (B, hkv, page_table.shape[1] * ps)
+    kp, vp = rows_check(k, "k", shape, dt, index), rows_check(v, "v", shape, dt, index)
     if new_lens is None:
         new_lens = torch.empty_like(lens)
-    ws = new_workspace(HEADER_BYTES, dev) if ws is None else check_workspace(ws, dev)
+    ws = new_workspace(HEADER_BYTES, k_cache.device) if ws is None else check_workspace(ws, index)
     strides = (ctypes.c_int64 * 6)(*k.stride()[:3], *v.stride()[:3])
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with on_device(dev):
-        st = _lib.bpt_cache_append(
-            c, kp, vp, T, strides,
-            None if counts is None else check(counts, "counts", (B,), torch.int32, dev),
-            check(new_lens, "new_lens", (B,), torch.int32, dev),
-            None if acc is None else check(acc, "acc", slots, torch.float32, dev),
-            None if pos is None else check(pos, "pos", slots, torch.int32, dev),
-            None if seen is None else check(seen, "seen", (B,), torch.int32, dev),
-            ws.data_ptr(), ws.numel(), s.cuda_stream)
+    st = run(_lib.bpt_cache_append, index, c, kp, vp, T, strides,
+             None if counts is None else check(counts, "counts", (B,), torch.int32, index),
+             check(new_lens, "new_lens", (B,), torch.int32, index),
+             None if acc is None else check(acc, "acc", slots, torch.float32, index),
+             None if pos is None else check(pos, "pos", slots, torch.int32, index),
+             None if seen is None else check(seen, "seen", (B,), torch.int32, index),
+             ws.data_ptr(), ws.numel(), stream_of(stream, index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_cache_append")
     return new_lens
@@ -161,28 +164,28 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     cache; returns out [B, heads, d_k].  With acc, the weight every slot
     received is added: acc_out = acc + weights (acc_out None: in place)."""
     c = _cache(k_cache, v_cache, page_table, lens)
-    dev, B = k_cache.device, c.batch
+    index, dt, B = k_cache.get_device(), k_cache.dtype, lens.shape[0]
     if q.dim() != 3:
         raise ValueError("q must be [B, heads, d_k]")
+    _, hkv, ps, dk = k_cache.shape
     h = q.shape[1]
-    qp = rows_check(q, "q", (B, h, c.d_k), k_cache.dtype, dev)
+    shape = (B, h, dk)
+    qp = rows_check(q, "q", shape, dt, index)
     if out is None:
-        out = torch.empty((B, h, c.d_k), dtype=q.dtype, device=dev)
-    op = rows_check(out, "out", (B, h, c.d_k), k_cache.dtype, dev)
+        out = torch.empty(shape, dtype=dt, device=q.device)
+    op = rows_check(out, "out", shape, dt, index)
     ap = aop = None
     if acc is not None:
-        slots = (B, c.kv_heads, c.max_pages * c.page_size)
-        ap = check(acc, "acc", slots, torch.float32, dev)
-        aop = ap if acc_out is None else check(acc_out, "acc_out", slots, torch.float32, dev)
+        slots = (B, hkv, page_table.shape[1] * ps)
+        ap = check(acc, "acc", slots, torch.float32, index)
+        aop = ap if acc_out is None else check(acc_out, "acc_out", slots, torch.float32, index)
     elif acc_out is not None:
         raise ValueError("acc_out without acc")
     ws = (attn_decode_workspace(q, k_cache, page_table, acc is not None) if ws is None
-          else check_workspace(ws, dev))
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with on_device(dev):
-        st = _lib.bpt_attn_decode(c, qp, h, q.stride(0), q.stride(1), window, sinks, ap, aop, op,
-                                  out.stride(0), out.stride(1), ws.data_ptr(), ws.numel(),
-                                  s.cuda_stream)
+          else check_workspace(ws, index))
+    st = run(_lib.bpt_attn_decode, index, c, qp, h, q.stride(0), q.stride(1), window, sinks, ap,
+             aop, op, out.stride(0), out.stride(1), ws.data_ptr(), ws.numel(),
+             stream_of(stream, index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_decode")
     return out
@@ -199,20 +202,18 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.
     accumulated weights, and packs the rest; returns new_lens.  acc_out,
     pos_out, new_lens None: updated in place."""
     c = _cache(k_cache, v_cache, page_table, lens)
-    dev, B = k_cache.device, c.batch
-    slots = (B, c.kv_heads, c.max_pages * c.page_size)
-    ap = check(acc, "acc", slots, torch.float32, dev)
-    pp = check(pos, "pos", slots, torch.int32, dev)
-    aop = ap if acc_out is None else check(acc_out, "acc_out", slots, torch.float32, dev)
-    pop = pp if pos_out is None else check(pos_out, "pos_out", slots, torch.int32, dev)
+    index, B = k_cache.get_device(), lens.shape[0]
+    slots = (B, k_cache.shape[1], page_table.shape[1] * k_cache.shape[2])
+    ap = check(acc, "acc", slots, torch.float32, index)
+    pp = check(pos, "pos", slots, torch.int32, index)
+    aop = ap if acc_out is None else check(acc_out, "acc_out", slots, torch.float32, index)
+    pop = pp if pos_out is None else check(pos_out, "pos_out", slots, torch.int32, index)
     new_lens = lens if new_lens is None else new_lens
-    ws = cache_workspace(k_cache, page_table) if ws is None else check_workspace(ws, dev)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with on_device(dev):
-        st = _lib.bpt_cache_evict(c, budget, recent, sinks, ap, pp,
-                                  check(seen, "seen", (B,), torch.int32, dev), aop, pop,
-                                  check(new_lens, "new_lens", (B,), torch.int32, dev),
-                                  ws.data_ptr(), ws.numel(), s.cuda_stream)
+    ws = cache_workspace(k_cache, page_table) if ws is None else check_workspace(ws, index)
+    st = run(_lib.bpt_cache_evict, index, c, budget, recent, sinks, ap, pp,
+             check(seen, "seen", (B,), torch.int32, index), aop, pop,
+             check(new_lens, "new_lens", (B,), torch.int32, index), ws.data_ptr(), ws.numel(),
+             stream_of(stream, index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_cache_evict")
     return new_lens

@@ -43,9 +43,15 @@
 
 namespace bpt {
 
-constexpr int kWinBwdThreads = 384;  // TMA, UMMA, TMEM owner, idle; 8 elementwise warps
-// 16-column groups (of eight) whose exp2 runs on the FMA pipe (unmasked tiles)
-constexpr uint32_t kWinBwdPolyGroups = 0x88u;
+// Warps: TMA, UMMA, TMEM owner, row terms (dK/dV only); then 16 elementwise warps, four
+// per scheduler, each with 32 rows and 32 columns of a tile: with 8 warps of
+// 64 columns the phases took twice what the tensor cores need (two warps per
+// scheduler do not cover their own latencies).
+constexpr int kWinBwdElem = 512;
+constexpr int kWinBwdThreads = 128 + kWinBwdElem;
+// Of every kWinBwdPolyEvery columns, kWinBwdPolyPairs pairs take their exp2
+// from a cubic on the FMA pipe (tiles without a mask).
+constexpr int kWinBwdPolyEvery = 16, kWinBwdPolyPairs = 3;
 
 struct WindowBwdParams {
   int nq, nkv, h, hkv, g, nqb, nblk;
@@ -172,43 +178,41 @@ __global__ void __launch_bounds__(256) window_terms_kernel(const WindowTermsPara
 }
 
 // --------------------------------------------------------- elementwise parts --
-// P of 32 columns (fp16 / bf16 pairs) from the scores: 2^(S c + a), a per
-// column pair from `col` or one for the row.
-template <typename T, uint32_t POLY, typename F>
-__device__ __forceinline__ void win_p32(const uint32_t (&sr)[32], uint32_t* pp, float c, F&& term,
-                                        int cc, uint32_t vis, bool masked) {
+// P of 32 columns from the scores, 2^(S c + a): kept in fp32 for dS (rounding
+// it twice there would show), rounded once for the product with dO.
+template <typename T, bool FULL, typename F>
+__device__ __forceinline__ void win_p32(uint32_t (&sr)[32], uint32_t (&pk)[16], float c, F&& term,
+                                        uint32_t vis) {
   const float2 c2 = make_float2(c, c);
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
     const float2 x =
         __ffma2_rn(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, term(k));
     float2 e;
-    if constexpr (POLY != 0) {
-      if ((POLY >> (2 * cc + (k >> 4))) & 1u)
-        e = exp2_poly2(x);
-      else
-        e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-    } else {
+    if (FULL && (k & (kWinBwdPolyEvery - 1)) >= kWinBwdPolyEvery - kWinBwdPolyPairs * 2)
+      e = exp2_poly2(x);
+    else
       e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      if (masked) {
-        if (!((vis >> k) & 1u)) e.x = 0.f;
-        if (!((vis >> (k + 1)) & 1u)) e.y = 0.f;
-      }
+    if constexpr (!FULL) {
+      if (!((vis >> k) & 1u)) e.x = 0.f;
+      if (!((vis >> (k + 1)) & 1u)) e.y = 0.f;
     }
-    pp[k >> 1] = pack16<T>(e.x, e.y);
+    sr[k] = __float_as_uint(e.x);
+    sr[k + 1] = __float_as_uint(e.y);
+    pk[k >> 1] = pack16<T>(e.x, e.y);
   }
 }
 // dS = P (dP sig + nd) of 32 columns.
-template <typename T, bool MASKED, typename F>
-__device__ __forceinline__ void win_ds32(const uint32_t (&dr)[32], const uint32_t* pp, uint32_t* ds,
-                                         float sig, F&& nd, uint32_t vis) {
+template <typename T, bool FULL, typename F>
+__device__ __forceinline__ void win_ds32(const uint32_t (&dr)[32], const uint32_t (&pr)[32],
+                                         uint32_t (&ds)[16], float sig, F&& nd, uint32_t vis) {
   const float2 s2 = make_float2(sig, sig);
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
     float2 v = __fmul2_rn(
-        unpack16<T>(pp[k >> 1]),
+        make_float2(__uint_as_float(pr[k]), __uint_as_float(pr[k + 1])),
         __ffma2_rn(make_float2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1])), s2, nd(k)));
-    if constexpr (MASKED) {  // 0 x (a value that is not finite) is not 0
+    if constexpr (!FULL) {  // 0 x (a value that is not finite) is not 0
       if (!((vis >> k) & 1u)) v.x = 0.f;
       if (!((vis >> (k + 1)) & 1u)) v.y = 0.f;
     }
@@ -216,20 +220,21 @@ __device__ __forceinline__ void win_ds32(const uint32_t (&dr)[32], const uint32_
   }
 }
 
-__device__ __forceinline__ void elementwise_sync() {
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-}
-
 template <int D>
 struct WindowBwdCfg {
   static constexpr int TILE = 128 * D * 2;
   static constexpr int CHUNK = 128 * 128;
-  // dK/dV: K, V, a ring of (Q, dO), two buffers of row terms
-  static constexpr int KV_SLOTS = D == 128 ? 2 : 4;
-  static constexpr int KV_OFF_RING = 2 * TILE;
-  static constexpr int KV_OFF_TERMS = KV_OFF_RING + KV_SLOTS * 2 * TILE;
-  static constexpr int KV_OFF_BAR = KV_OFF_TERMS + 2 * 2 * 128 * 4;
-  static constexpr int KV_SMEM = KV_OFF_BAR + 256 + 1024;
+  // dK/dV: K, V, rings of Q (held from S_t to dK_t: three, so that the next
+  // load never waits for a product in flight), dO (dP_t to dV_t) and row terms.
+  // The barriers and shared words live behind them: with d_k = 128 the block
+  // has no room for padding, so it has no static shared memory and its dynamic
+  // part starts on the 1024-byte boundary that the swizzle needs.
+  static constexpr int Q_SLOTS = D == 128 ? 3 : 4, DO_SLOTS = D == 128 ? 2 : 3, TERM_SLOTS = 2;
+  static constexpr int KV_OFF_Q = 2 * TILE;
+  static constexpr int KV_OFF_DO = KV_OFF_Q + Q_SLOTS * TILE;
+  static constexpr int KV_OFF_TERMS = KV_OFF_DO + DO_SLOTS * TILE;
+  static constexpr int KV_OFF_BAR = KV_OFF_TERMS + TERM_SLOTS * 2 * 128 * 4;
+  static constexpr int KV_SMEM = KV_OFF_BAR + 512;
   // dQ: Q, dO, rings of K (held until dQ_j) and V (until dP_j)
   static constexpr int QK_SLOTS = 3, QV_SLOTS = 2;
   static constexpr int Q_OFF_K = 2 * TILE;
@@ -237,17 +242,22 @@ struct WindowBwdCfg {
   static constexpr int Q_OFF_BAR = Q_OFF_V + QV_SLOTS * TILE;
   static constexpr int Q_SMEM = Q_OFF_BAR + 256 + 1024;
   static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D;
-  static constexpr uint32_t TQ_S = 0, TQ_DP = 256, TQ_A = 384;
+  // dQ: one score buffer (free once its tile is in registers), two of dP / dS
+  static constexpr uint32_t TQ_S = 0, TQ_DP = 128, TQ_A = 384;
   static_assert(KV_SMEM <= 232448 && Q_SMEM <= 232448, "shared memory");
 };
 
-// A 128-row product with A from tensor memory, the two 32-column chunks of
-// one half of A's columns.
+// A 128-row product with A from tensor memory, 64 columns of A: the packed
+// pairs of columns 32 c .. lie in words 32 c .. 32 c + 15.
 template <int D>
 __device__ __forceinline__ void win_issue_ts_half(uint32_t d, uint32_t a, uint32_t b_lo,
                                                   uint32_t idesc, int half, bool first) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) bwd_issue_ts_chunk<D>(d, a, b_lo, idesc, 2 * half + q, first);
+  for (int q = 0; q < 4; ++q) {
+    const int k = 4 * half + q;
+    umma_ts(d, a + 32 * (k >> 1) + 8 * (k & 1), b_lo + ((k * 2048) >> 4), sdesc_hi(1024), idesc,
+            (!first || k > 0) ? 1u : 0u);
+  }
 }
 
 // Eight consecutive values of a row as 16 bytes.
@@ -268,22 +278,32 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
                          const __grid_constant__ CUtensorMap mapV,
                          const __grid_constant__ CUtensorMap mapDO, const WindowBwdParams p) {
   using C = WindowBwdCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t win_smem[];
+  uint8_t* smem = win_smem;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::KV_OFF_BAR);
   const uint32_t kv_full = smem_u32(bars + 0);
-  const uint32_t ring_full0 = smem_u32(bars + 1);
-  const uint32_t ring_empty0 = smem_u32(bars + 5);
-  const uint32_t s_full = smem_u32(bars + 9);
-  const uint32_t dp_full = smem_u32(bars + 10);
-  const uint32_t p_half0 = smem_u32(bars + 11);   // [2]
-  const uint32_t ds_half0 = smem_u32(bars + 13);  // [2]
-  const uint32_t acc_done = smem_u32(bars + 15);
-  const uint32_t drain = smem_u32(bars + 16);
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-  __shared__ int plan_sh[3];  // key block, part, first slot of its parts (-1: not cut)
+  const uint32_t q_full0 = smem_u32(bars + 1);
+  const uint32_t q_empty0 = smem_u32(bars + 5);
+  const uint32_t do_full0 = smem_u32(bars + 9);
+  const uint32_t do_empty0 = smem_u32(bars + 12);
+  const uint32_t s_full = smem_u32(bars + 15);
+  const uint32_t dp_full = smem_u32(bars + 16);
+  const uint32_t p_half0 = smem_u32(bars + 17);   // [2]
+  const uint32_t ds_half0 = smem_u32(bars + 19);  // [2]
+  const uint32_t acc_done = smem_u32(bars + 21);
+  const uint32_t drain = smem_u32(bars + 22);
+  const uint32_t terms_full0 = smem_u32(bars + 23);   // [2]
+  const uint32_t terms_empty0 = smem_u32(bars + 25);  // [2]
+  // shared words: TMEM base, abort flag, plan (key block, part, first slot of
+  // its parts or -1 if the block is not cut)
+  int* words = reinterpret_cast<int*>(bars + 28);
+  uint32_t* tmem_base_p = reinterpret_cast<uint32_t*>(words);
+  int* abort_p = words + 1;
+  int* plan_sh = words + 2;
+  if ((smem_u32(smem) & 1023u) != 0) {  // (every thread: the swizzle would not match)
+    record_error(p.err, kErrTimeout, kSiteAttnProducer);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bk = blockIdx.y;
   const int bidx = bk / p.hkv, kvh = bk - bidx * p.hkv;
@@ -321,30 +341,38 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   }
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < C::KV_SLOTS; ++s) {
-      mbar_init(ring_full0 + 8 * s, 1);
-      mbar_init(ring_empty0 + 8 * s, 1);
+    for (int s = 0; s < C::Q_SLOTS; ++s) {
+      mbar_init(q_full0 + 8 * s, 1);
+      mbar_init(q_empty0 + 8 * s, 1);
+    }
+    for (int s = 0; s < C::DO_SLOTS; ++s) {
+      mbar_init(do_full0 + 8 * s, 1);
+      mbar_init(do_empty0 + 8 * s, 1);
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     for (int c = 0; c < 2; ++c) {
-      mbar_init(p_half0 + 8 * c, 4);
-      mbar_init(ds_half0 + 8 * c, 4);
+      mbar_init(p_half0 + 8 * c, 8);
+      mbar_init(ds_half0 + 8 * c, 8);
+    }
+    for (int c = 0; c < C::TERM_SLOTS; ++c) {
+      mbar_init(terms_full0 + 8 * c, 1);
+      mbar_init(terms_empty0 + 8 * c, 16);
     }
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
-    abort_sh = 0;
+    *abort_p = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(&tmem_base_sh), 512);
+    tmem_alloc(smem_u32(tmem_base_p), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
-  volatile int* abort_flag = &abort_sh;
+  const uint32_t tmem = *tmem_base_p;
+  volatile int* abort_flag = abort_p;
   const int jb = plan_sh[0], part = plan_sh[1], slot0 = plan_sh[2];
   const int kb = jb * 128;
   const WindowQueries wq = window_queries(p.nq, p.nkv, p.window, p.sinks, kb, len - off);
@@ -360,8 +388,9 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     // ------------------------------------------------------------ producer
     const bool leader = elect_one();
     if (n_it > 0) {
-      int armed[C::KV_SLOTS];
-      for (int s = 0; s < C::KV_SLOTS; ++s) armed[s] = -1;
+      int q_armed[C::Q_SLOTS], do_armed[C::DO_SLOTS];
+      for (int s = 0; s < C::Q_SLOTS; ++s) q_armed[s] = -1;
+      for (int s = 0; s < C::DO_SLOTS; ++s) do_armed[s] = -1;
       if (leader) {
         mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
         tma_load_5d(smem_u32(smem), &mapK, kv_full, 0, kb, 0, kvh, bidx);
@@ -369,17 +398,25 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       }
       int hl = hl0, tl = tl0;
       for (int t = 0; t < n_it; ++t) {
-        const int s = t % C::KV_SLOTS;
-        const uint32_t phase = static_cast<uint32_t>((t / C::KV_SLOTS) & 1);
-        if (!mbar_wait_warp(ring_empty0 + 8 * s, phase ^ 1u, abort_flag, p.err, kSiteAttnProducer))
+        const int qs = t % C::Q_SLOTS, ds = t % C::DO_SLOTS;
+        const uint32_t qph = static_cast<uint32_t>((t / C::Q_SLOTS) & 1);
+        const uint32_t dph = static_cast<uint32_t>((t / C::DO_SLOTS) & 1);
+        if (!mbar_wait_warp(q_empty0 + 8 * qs, qph ^ 1u, abort_flag, p.err, kSiteAttnProducer))
           break;
-        armed[s] = static_cast<int>(phase);
+        q_armed[qs] = static_cast<int>(qph);
         if (leader) {
-          const uint32_t dst = smem_u32(smem + C::KV_OFF_RING + s * 2 * C::TILE);
-          mbar_arrive_expect_tx(ring_full0 + 8 * s, 2 * C::TILE);
-          tma_load_5d(dst, &mapQ, ring_full0 + 8 * s, 0, t0 + 128 * tl, 0, kvh * p.g + hl, bidx);
-          tma_load_5d(dst + C::TILE, &mapDO, ring_full0 + 8 * s, 0, t0 + 128 * tl, 0,
-                      kvh * p.g + hl, bidx);
+          mbar_arrive_expect_tx(q_full0 + 8 * qs, C::TILE);
+          tma_load_5d(smem_u32(smem + C::KV_OFF_Q + qs * C::TILE), &mapQ, q_full0 + 8 * qs, 0,
+                      t0 + 128 * tl, 0, kvh * p.g + hl, bidx);
+        }
+        __syncwarp();
+        if (!mbar_wait_warp(do_empty0 + 8 * ds, dph ^ 1u, abort_flag, p.err, kSiteAttnProducer))
+          break;
+        do_armed[ds] = static_cast<int>(dph);
+        if (leader) {
+          mbar_arrive_expect_tx(do_full0 + 8 * ds, C::TILE);
+          tma_load_5d(smem_u32(smem + C::KV_OFF_DO + ds * C::TILE), &mapDO, do_full0 + 8 * ds, 0,
+                      t0 + 128 * tl, 0, kvh * p.g + hl, bidx);
         }
         __syncwarp();
         if (++tl == tiles) {
@@ -388,9 +425,12 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
         }
       }
       mbar_wait_drain(kv_full, 0, p.err);
-      for (int s = 0; s < C::KV_SLOTS; ++s)
-        if (armed[s] >= 0)
-          mbar_wait_drain(ring_full0 + 8 * s, static_cast<uint32_t>(armed[s]), p.err);
+      for (int s = 0; s < C::Q_SLOTS; ++s)
+        if (q_armed[s] >= 0)
+          mbar_wait_drain(q_full0 + 8 * s, static_cast<uint32_t>(q_armed[s]), p.err);
+      for (int s = 0; s < C::DO_SLOTS; ++s)
+        if (do_armed[s] >= 0)
+          mbar_wait_drain(do_full0 + 8 * s, static_cast<uint32_t>(do_armed[s]), p.err);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- UMMA issue
@@ -403,25 +443,31 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       if (leader) umma_commit(bar);
       __syncwarp();
     };
-    auto slot_of = [&](int t) {
-      return smem_u32(smem + C::KV_OFF_RING + (t % C::KV_SLOTS) * 2 * C::TILE);
+    auto q_slot = [&](int t) { return smem_u32(smem + C::KV_OFF_Q + (t % C::Q_SLOTS) * C::TILE); };
+    auto do_slot = [&](int t) {
+      return smem_u32(smem + C::KV_OFF_DO + (t % C::DO_SLOTS) * C::TILE);
     };
     auto issue_s = [&](int t) -> bool {
-      if (!mbar_wait_warp(ring_full0 + 8 * (t % C::KV_SLOTS),
-                          static_cast<uint32_t>((t / C::KV_SLOTS) & 1), abort_flag, p.err,
+      if (!mbar_wait_warp(q_full0 + 8 * (t % C::Q_SLOTS),
+                          static_cast<uint32_t>((t / C::Q_SLOTS) & 1), abort_flag, p.err,
                           kSiteAttnMma))
         return false;
       tc_fence_after();
-      if (leader) bwd_issue_ss<D>(tmem + C::TM_S, k_lo, sdesc_lo(slot_of(t), 16), idesc_s);
+      if (leader) bwd_issue_ss<D>(tmem + C::TM_S, k_lo, sdesc_lo(q_slot(t), 16), idesc_s);
       __syncwarp();
       commit(s_full);
       return true;
     };
-    auto issue_dp = [&](int t) {
-      if (leader)
-        bwd_issue_ss<D>(tmem + C::TM_DP, v_lo, sdesc_lo(slot_of(t) + C::TILE, 16), idesc_s);
+    auto issue_dp = [&](int t) -> bool {
+      if (!mbar_wait_warp(do_full0 + 8 * (t % C::DO_SLOTS),
+                          static_cast<uint32_t>((t / C::DO_SLOTS) & 1), abort_flag, p.err,
+                          kSiteAttnMma))
+        return false;
+      tc_fence_after();
+      if (leader) bwd_issue_ss<D>(tmem + C::TM_DP, v_lo, sdesc_lo(do_slot(t), 16), idesc_s);
       __syncwarp();
       commit(dp_full);
+      return true;
     };
     auto issue_grad = [&](int t, uint32_t bar0, uint32_t acc, uint32_t a_tm, uint32_t b_lo) {
       for (int hh = 0; hh < 2; ++hh) {
@@ -434,113 +480,121 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       }
       return true;
     };
-    bool ok = n_it > 0 && mbar_wait_warp(kv_full, 0, abort_flag, p.err, kSiteAttnMma) && issue_s(0);
-    if (ok) issue_dp(0);
+    bool ok = n_it > 0 && mbar_wait_warp(kv_full, 0, abort_flag, p.err, kSiteAttnMma) &&
+              issue_s(0) && issue_dp(0);
     for (int t = 0; t < n_it && ok; ++t) {
-      const uint32_t sl = slot_of(t);
       // dV += P^T dO_t; then S^T_t has been read in full: the next scores go there
       if (!(ok = issue_grad(t, p_half0, tmem + C::TM_DV, tmem + C::TM_S,
-                            sdesc_lo(sl + C::TILE, C::CHUNK))))
+                            sdesc_lo(do_slot(t), C::CHUNK))))
         break;
+      commit(do_empty0 + 8 * (t % C::DO_SLOTS));
       if (t + 1 < n_it && !(ok = issue_s(t + 1))) break;
-      // dK += dS^T Q_t
-      if (!(ok = issue_grad(t, ds_half0, tmem + C::TM_DK, tmem + C::TM_DP, sdesc_lo(sl, C::CHUNK))))
+      // dK += dS^T Q_t; then dP^T_t has been read
+      if (!(ok = issue_grad(t, ds_half0, tmem + C::TM_DK, tmem + C::TM_DP,
+                            sdesc_lo(q_slot(t), C::CHUNK))))
         break;
-      commit(ring_empty0 + 8 * (t % C::KV_SLOTS));
-      if (t + 1 < n_it) issue_dp(t + 1);
+      commit(q_empty0 + 8 * (t % C::Q_SLOTS));
+      if (t + 1 < n_it) ok = issue_dp(t + 1);
     }
     commit(acc_done);
     commit(drain);
     mbar_wait_drain(drain, 0, p.err);
+  } else if (warp == 3) {
+    // ----------------------------------------------------------- row terms
+    const float sig = grad_sigma(p.amax) * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
+    const float2* rows = p.terms + (static_cast<long long>(bidx) * p.h + kvh * p.g + hl0) * p.nq;
+    int tl = tl0;
+    for (int t = 0; t < n_it; ++t) {
+      const int ts = t % C::TERM_SLOTS;
+      float2 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = t0 + 128 * tl + lane + 32 * k;
+        v[k] = i >= 0 ? __ldg(rows + i) : make_float2(-INFINITY, 0.f);
+      }
+      if (!mbar_wait_warp(terms_empty0 + 8 * ts,
+                          static_cast<uint32_t>((t / C::TERM_SLOTS) & 1) ^ 1u, abort_flag, p.err,
+                          kSiteAttnProducer))
+        break;
+      float* st = reinterpret_cast<float*>(smem + C::KV_OFF_TERMS) + ts * 256;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        st[lane + 32 * k] = v[k].x;
+        st[128 + lane + 32 * k] = v[k].y * sig;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(terms_full0 + 8 * ts);
+      if (++tl == tiles) {
+        tl = 0;
+        rows += p.nq;
+      }
+    }
   } else if (warp >= 4) {
     // --------------------------------------------------------- elementwise
-    const int e = warp & 3, half = (warp - 4) >> 2, tt = threadIdx.x - 128;
+    const int e = warp & 3, cc = (warp - 4) >> 2;  // columns 32 cc ..
     const int kr = e * 32 + lane, key = kb + kr;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
     const float c = p.scale * kLog2e;
     const float sigma = grad_sigma(p.amax);
     const float sig = sigma * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
-    float* terms_sh = reinterpret_cast<float*>(smem + C::KV_OFF_TERMS);  // [2][a: 128, nd: 128]
-    int hl = hl0, tl = tl0;
-    auto load_terms = [&]() {
-      const int i = t0 + 128 * tl + tt;
-      return i >= 0 ? __ldg(p.terms + (static_cast<long long>(bidx) * p.h + kvh * p.g + hl) * p.nq + i)
-                    : make_float2(-INFINITY, 0.f);
-    };
-    float2 next = make_float2(-INFINITY, 0.f);
-    if (n_it > 0 && tt < 128) next = load_terms();
-    // After a wait that ran out the loop goes on, without work, so that all
-    // eight warps meet at every barrier.
+    int tl = tl0;
     bool ok = n_it > 0;
-    for (int t = 0; t < n_it; ++t) {
-      float* st = terms_sh + (t & 1) * 256;
-      if (tt < 128) {
-        st[tt] = next.x;
-        st[128 + tt] = next.y * sig;
-      }
-      elementwise_sync();  // (everyone is past tile t - 1, so past reading this buffer)
+    for (int t = 0; t < n_it && ok; ++t) {
+      const int ts = t % C::TERM_SLOTS;
+      const float* st = reinterpret_cast<const float*>(smem + C::KV_OFF_TERMS) + ts * 256;
       const int pq = off + t0 + 128 * tl;  // position of the tile's first query
-      if (++tl == tiles) {
-        tl = 0;
-        ++hl;
-      }
-      if (tt < 128 && t + 1 < n_it) next = load_terms();
+      if (++tl == tiles) tl = 0;
       const uint32_t ph = static_cast<uint32_t>(t & 1);
-      if (ok) ok = mbar_wait_warp(s_full, ph, abort_flag, p.err, kSiteAttnSoftmax);
+      if (!mbar_wait_warp(terms_full0 + 8 * ts, static_cast<uint32_t>((t / C::TERM_SLOTS) & 1),
+                          abort_flag, p.err, kSiteAttnSoftmax) ||
+          !mbar_wait_warp(s_full, ph, abort_flag, p.err, kSiteAttnSoftmax)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       // every key of the block is seen by every query of the tile
       const bool full = pq >= kb + 127 && (pq + 127 < kb + p.window || kb + 128 <= p.sinks);
       const int q_lo = key - pq, q_hi = key < p.sinks ? 128 : key + p.window - pq;
-      uint32_t pp[32], vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-      if (ok) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int cc = 2 * half + u;
-          uint32_t sr[32];
-          tmem_ld_32x32b_x32(t_lane + C::TM_S + cc * 32, sr);
-          tmem_ld_wait();
-          auto term = [&](int k) { return *reinterpret_cast<const float2*>(st + cc * 32 + k); };
-          if (full) {
-            if (u == 0)
-              win_p32<T, kWinBwdPolyGroups>(sr, pp, c, term, 0, 0u, false);
-            else
-              win_p32<T, kWinBwdPolyGroups>(sr, pp + 16, c, term, 1, 0u, false);
-          } else {
-            vis[u] = bits_range(q_lo, q_hi, cc);
-            win_p32<T, 0u>(sr, pp + 16 * u, c, term, u, vis[u], true);
-          }
-          tmem_st16(t_lane + C::TM_S + packed_col(cc), pp + 16 * u);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_half0 + 8 * half);
-        ok = mbar_wait_warp(dp_full, ph, abort_flag, p.err, kSiteAttnSoftmax);
+      const uint32_t vis = full ? 0xFFFFFFFFu : bits_range(q_lo, q_hi, cc);
+      uint32_t pr[32], pk[16];
+      tmem_ld_32x32b_x32(t_lane + C::TM_S + cc * 32, pr);
+      tmem_ld_wait();
+      auto term = [&](int k) { return *reinterpret_cast<const float2*>(st + cc * 32 + k); };
+      if (full)
+        win_p32<T, true>(pr, pk, c, term, vis);
+      else
+        win_p32<T, false>(pr, pk, c, term, vis);
+      tmem_st16(t_lane + C::TM_S + cc * 32, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_half0 + 8 * (cc >> 1));
+      if (!mbar_wait_warp(dp_full, ph, abort_flag, p.err, kSiteAttnSoftmax)) {
+        ok = false;
+        break;
       }
       tc_fence_after();
-      if (ok) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int cc = 2 * half + u;
-          uint32_t dr[32], ds[16];
-          tmem_ld_32x32b_x32(t_lane + C::TM_DP + cc * 32, dr);
-          tmem_ld_wait();
-          auto nd = [&](int k) { return *reinterpret_cast<const float2*>(st + 128 + cc * 32 + k); };
-          if (full)
-            win_ds32<T, false>(dr, pp + 16 * u, ds, sig, nd, 0u);
-          else
-            win_ds32<T, true>(dr, pp + 16 * u, ds, sig, nd, vis[u]);
-          tmem_st16(t_lane + C::TM_DP + packed_col(cc), ds);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ds_half0 + 8 * half);
+      uint32_t dr[32];
+      tmem_ld_32x32b_x32(t_lane + C::TM_DP + cc * 32, dr);
+      tmem_ld_wait();
+      auto nd = [&](int k) { return *reinterpret_cast<const float2*>(st + 128 + cc * 32 + k); };
+      if (full)
+        win_ds32<T, true>(dr, pr, pk, sig, nd, vis);
+      else
+        win_ds32<T, false>(dr, pr, pk, sig, nd, vis);
+      tmem_st16(t_lane + C::TM_DP + cc * 32, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ds_half0 + 8 * (cc >> 1));
+        mbar_arrive(terms_empty0 + 8 * ts);
       }
     }
     const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
     tc_fence_after();
-    // half 0 stores dV, half 1 dK
+    // even column groups store dV, odd ones dK, each half of the columns
+    const int half = cc & 1, c0 = (cc >> 1) * (D / 64), c1 = c0 + D / 64;
     const float f = half == 0 ? exp2f(-WinScale<T>::kP) : p.scale / (sigma * WinScale<T>::kDS);
     const uint32_t acc = t_lane + (half == 0 ? C::TM_DV : C::TM_DK);
     if (slot0 >= 0) {
@@ -548,13 +602,13 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
         float* dst = p.part + ((static_cast<long long>(bk) * p.split_parts + slot0 + part) * 2 + half) *
                                   (128 * D) + kr * D;
 #pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
+        for (int x = c0; x < c1; ++x) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(acc + cc * 32, v);
+          tmem_ld_32x32b_x32(acc + x * 32, v);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(dst + cc * 32 + k) =
+            *reinterpret_cast<float4*>(dst + x * 32 + k) =
                 make_float4(__uint_as_float(v[k]) * f, __uint_as_float(v[k + 1]) * f,
                             __uint_as_float(v[k + 2]) * f, __uint_as_float(v[k + 3]) * f);
         }
@@ -564,17 +618,17 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
                    ? static_cast<T*>(p.dv) + bidx * p.dv_b + key * p.dv_n + kvh * p.dv_h
                    : static_cast<T*>(p.dk) + bidx * p.dk_b + key * p.dk_n + kvh * p.dk_h;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
+      for (int x = c0; x < c1; ++x) {
         uint32_t v[32];
         if (done) {
-          tmem_ld_32x32b_x32(acc + cc * 32, v);
+          tmem_ld_32x32b_x32(acc + x * 32, v);
           tmem_ld_wait();
         }
         if (key >= p.nkv) continue;
         const bool zero = !done || key >= len;  // no query sees the key
 #pragma unroll
         for (int k = 0; k < 32; k += 8)
-          *reinterpret_cast<uint4*>(dst + cc * 32 + k) =
+          *reinterpret_cast<uint4*>(dst + x * 32 + k) =
               zero ? make_uint4(0u, 0u, 0u, 0u) : win_pack8<T>(v + k, f);
       }
     }
@@ -645,12 +699,12 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   const uint32_t k_empty0 = smem_u32(bars + 4);  // [3]
   const uint32_t v_full0 = smem_u32(bars + 7);   // [2]
   const uint32_t v_empty0 = smem_u32(bars + 9);  // [2]
-  const uint32_t s_full0 = smem_u32(bars + 11);  // [2]: S_j landed in buffer j % 2
-  const uint32_t s_free0 = smem_u32(bars + 13);  // [2]: buffer j % 2 read by every warp
-  const uint32_t dp_full = smem_u32(bars + 15);
-  const uint32_t ds_half0 = smem_u32(bars + 16);  // [2]
-  const uint32_t acc_done = smem_u32(bars + 18);
-  const uint32_t drain = smem_u32(bars + 19);
+  const uint32_t s_full = smem_u32(bars + 11);
+  const uint32_t s_free = smem_u32(bars + 12);    // S_j is in every warp's registers
+  const uint32_t dp_full0 = smem_u32(bars + 13);  // [2], by j % 2
+  const uint32_t ds_half0 = smem_u32(bars + 15);  // [2][2]: by j % 2, columns 0..63 / 64..127
+  const uint32_t acc_done = smem_u32(bars + 19);
+  const uint32_t drain = smem_u32(bars + 20);
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -673,12 +727,10 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       mbar_init(v_full0 + 8 * s, 1);
       mbar_init(v_empty0 + 8 * s, 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(s_full0 + 8 * b, 1);
-      mbar_init(s_free0 + 8 * b, 8);
-      mbar_init(ds_half0 + 8 * b, 4);
-    }
-    mbar_init(dp_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 16);
+    for (int b = 0; b < 2; ++b) mbar_init(dp_full0 + 8 * b, 1);
+    for (int b = 0; b < 4; ++b) mbar_init(ds_half0 + 8 * b, 8);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     abort_sh = 0;
@@ -757,11 +809,9 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
                           kSiteAttnMma))
         return false;
       tc_fence_after();
-      if (leader)
-        bwd_issue_ss<D>(tmem + C::TQ_S + 128u * static_cast<uint32_t>(j & 1), q_lo,
-                        sdesc_lo(k_slot(j), 16), idesc_s);
+      if (leader) bwd_issue_ss<D>(tmem + C::TQ_S, q_lo, sdesc_lo(k_slot(j), 16), idesc_s);
       __syncwarp();
-      commit(s_full0 + 8 * (j & 1));
+      commit(s_full);
       return true;
     };
     auto issue_dp = [&](int j) -> bool {
@@ -770,47 +820,48 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
                           kSiteAttnMma))
         return false;
       tc_fence_after();
-      if (leader) bwd_issue_ss<D>(tmem + C::TQ_DP, do_lo, sdesc_lo(v_slot(j), 16), idesc_s);
+      if (leader)
+        bwd_issue_ss<D>(tmem + C::TQ_DP + 128u * static_cast<uint32_t>(j & 1), do_lo,
+                        sdesc_lo(v_slot(j), 16), idesc_s);
       __syncwarp();
-      commit(dp_full);
+      commit(dp_full0 + 8 * (j & 1));
       commit(v_empty0 + 8 * (j % C::QV_SLOTS));
       return true;
     };
     bool ok = n_kv > 0 && mbar_wait_warp(q_full, 0, abort_flag, p.err, kSiteAttnMma) &&
-              issue_s(0) && issue_dp(0) && (n_kv < 2 || issue_s(1));
+              issue_s(0) && issue_dp(0);
     for (int j = 0; j < n_kv && ok; ++j) {
+      if (j + 1 < n_kv) {
+        // S_j+1 over S_j once that is in registers; dP_j+1 over dS_j-1, which
+        // dQ_j-1 (issued before) has read
+        ok = mbar_wait_warp(s_free, static_cast<uint32_t>(j & 1), abort_flag, p.err,
+                            kSiteAttnMma);
+        if (ok) tc_fence_after();
+        ok = ok && issue_s(j + 1) && issue_dp(j + 1);
+        if (!ok) break;
+      }
       for (int hh = 0; hh < 2; ++hh) {
-        if (!mbar_wait_warp(ds_half0 + 8 * hh, static_cast<uint32_t>(j & 1), abort_flag, p.err,
-                            kSiteAttnMma)) {
+        if (!mbar_wait_warp(ds_half0 + 16 * (j & 1) + 8 * hh, static_cast<uint32_t>((j >> 1) & 1),
+                            abort_flag, p.err, kSiteAttnMma)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (leader)
-          win_issue_ts_half<D>(tmem + C::TQ_A, tmem + C::TQ_DP, sdesc_lo(k_slot(j), C::CHUNK),
-                               idesc_o, hh, j == 0);
+          win_issue_ts_half<D>(tmem + C::TQ_A,
+                               tmem + C::TQ_DP + 128u * static_cast<uint32_t>(j & 1),
+                               sdesc_lo(k_slot(j), C::CHUNK), idesc_o, hh, j == 0);
         __syncwarp();
       }
       if (!ok) break;
       commit(k_empty0 + 8 * (j % C::QK_SLOTS));
-      // dP_j+1 overwrites dS_j: after dQ_j (in order) and after every warp's
-      // hand-over of dS_j (all of dP_j has been read)
-      if (j + 1 < n_kv && !(ok = issue_dp(j + 1))) break;
-      if (j + 2 < n_kv) {
-        if (!mbar_wait_warp(s_free0 + 8 * (j & 1), static_cast<uint32_t>((j >> 1) & 1), abort_flag,
-                            p.err, kSiteAttnMma) ||
-            !issue_s(j + 2)) {
-          ok = false;
-          break;
-        }
-      }
     }
     commit(acc_done);
     commit(drain);
     mbar_wait_drain(drain, 0, p.err);
   } else if (warp >= 4) {
     // --------------------------------------------------------- elementwise
-    const int e = warp & 3, half = (warp - 4) >> 2;
+    const int e = warp & 3, cc = (warp - 4) >> 2;  // columns 32 cc ..
     const int qr = e * 32 + lane, i = qb * 128 + qr, pos = p0 + qr;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
     const float c = p.scale * kLog2e;
@@ -823,80 +874,64 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     auto nd = [&](int) { return nd2; };
     bool ok = n_kv > 0;
     for (int j = 0; j < n_kv && ok; ++j) {
-      if (!mbar_wait_warp(s_full0 + 8 * (j & 1), static_cast<uint32_t>((j >> 1) & 1), abort_flag,
-                          p.err, kSiteAttnSoftmax)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const int kb = kt.key(j);
-      const bool sink = j < kt.n_s;
-      const bool full = !sink && kb + 127 <= p0 && kb >= kt.lo && kb >= p0 + 128 - p.window;
-      const uint32_t tS = t_lane + C::TQ_S + 128u * static_cast<uint32_t>(j & 1);
-      uint32_t pp[32], vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int cc = 2 * half + u;
-        uint32_t sr[32];
-        tmem_ld_32x32b_x32(tS + cc * 32, sr);
-        tmem_ld_wait();
-        if (u == 1) {
-          // this warp's scores of buffer j % 2 are in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free0 + 8 * (j & 1));
-        }
-        if (full) {
-          if (u == 0)
-            win_p32<T, kWinBwdPolyGroups>(sr, pp, c, term, 0, 0u, false);
-          else
-            win_p32<T, kWinBwdPolyGroups>(sr, pp + 16, c, term, 1, 0u, false);
-        } else {
-          vis[u] = sink ? bits_range(0, kt.ns - kb, cc)
-                        : window_bits(pos, kb, kt.lo, p.window, p.sinks, cc);
-          win_p32<T, 0u>(sr, pp + 16 * u, c, term, u, vis[u], true);
-        }
-      }
-      if (!mbar_wait_warp(dp_full, static_cast<uint32_t>(j & 1), abort_flag, p.err,
+      if (!mbar_wait_warp(s_full, static_cast<uint32_t>(j & 1), abort_flag, p.err,
                           kSiteAttnSoftmax)) {
         ok = false;
         break;
       }
       tc_fence_after();
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int cc = 2 * half + u;
-        uint32_t dr[32], ds[16];
-        tmem_ld_32x32b_x32(t_lane + C::TQ_DP + cc * 32, dr);
-        tmem_ld_wait();
-        if (full)
-          win_ds32<T, false>(dr, pp + 16 * u, ds, sig, nd, 0u);
-        else
-          win_ds32<T, true>(dr, pp + 16 * u, ds, sig, nd, vis[u]);
-        tmem_st16(t_lane + C::TQ_DP + packed_col(cc), ds);
+      uint32_t pr[32], pk[16];
+      tmem_ld_32x32b_x32(t_lane + C::TQ_S + cc * 32, pr);
+      const int kb = kt.key(j);
+      const bool sink = j < kt.n_s;
+      const bool full = !sink && kb + 127 <= p0 && kb >= kt.lo && kb >= p0 + 128 - p.window;
+      const uint32_t vis = full ? 0xFFFFFFFFu
+                           : sink ? bits_range(0, kt.ns - kb, cc)
+                                  : window_bits(pos, kb, kt.lo, p.window, p.sinks, cc);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free);
+      if (full)
+        win_p32<T, true>(pr, pk, c, term, vis);
+      else
+        win_p32<T, false>(pr, pk, c, term, vis);
+      if (!mbar_wait_warp(dp_full0 + 8 * (j & 1), static_cast<uint32_t>((j >> 1) & 1), abort_flag,
+                          p.err, kSiteAttnSoftmax)) {
+        ok = false;
+        break;
       }
+      tc_fence_after();
+      const uint32_t tP = t_lane + C::TQ_DP + 128u * static_cast<uint32_t>(j & 1) + cc * 32;
+      uint32_t dr[32];
+      tmem_ld_32x32b_x32(tP, dr);
+      tmem_ld_wait();
+      if (full)
+        win_ds32<T, true>(dr, pr, pk, sig, nd, vis);
+      else
+        win_ds32<T, false>(dr, pr, pk, sig, nd, vis);
+      tmem_st16(tP, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_half0 + 8 * half);
+      if (lane == 0) mbar_arrive(ds_half0 + 16 * (j & 1) + 8 * (cc >> 1));
     }
     const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
     tc_fence_after();
     const float f = p.scale / (sigma * WinScale<T>::kDS);
     T* dst = static_cast<T*>(p.dq) + bidx * p.dq_b + i * p.dq_n + head * p.dq_h;
-    // each half stores its half of the columns
-#pragma unroll 1
-    for (int cc = half * (D / 64); cc < (half + 1) * (D / 64); ++cc) {
+    // the column groups share the d_k / 32 pieces of the row
+    for (int x = cc; x < D / 32; x += 4) {
       uint32_t v[32];
       if (done) {
-        tmem_ld_32x32b_x32(t_lane + C::TQ_A + cc * 32, v);
+        tmem_ld_32x32b_x32(t_lane + C::TQ_A + x * 32, v);
         tmem_ld_wait();
       }
       if (i >= p.nq) continue;
       const bool zero = !done || pos >= len;
 #pragma unroll
       for (int k = 0; k < 32; k += 8)
-        *reinterpret_cast<uint4*>(dst + cc * 32 + k) =
+        *reinterpret_cast<uint4*>(dst + x * 32 + k) =
             zero ? make_uint4(0u, 0u, 0u, 0u) : win_pack8<T>(v + k, f);
     }
   }
