@@ -119,7 +119,7 @@ def attn_decode_workspace(q: torch.Tensor, k_cache: torch.Tensor, page_table: to
                                                      with_acc)
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_decode_workspace_size")
-    return new_workspace(nbytes, k_cache.device)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=k_cache.device)
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

@@ -11,17 +11,22 @@
 //    pairs, cut into equal runs, one per CTA (fewer runs if there are fewer tiles), whatever the lengths: a long
 //    sequence is split over many CTAs, short ones share one.  The lengths are
 //    read on the device, so no plan has to be made for a batch.
-//  - The query heads that share a kv head are the 16 rows of one warp MMA
-//    (m16n8k16), so each K/V row is read once for all of them.  (The legacy
-//    MMA is enough here: padded to 16 rows it needs ~110 TFLOP/s at full HBM
-//    rate, and a tcgen05 tile would pad to 128.)
+//  - The query heads that share a kv head are the 8 columns of one warp MMA
+//    (m16n8k16; two of them for more than 8 heads) whose 16 rows are slots:
+//    S^T = K Q^T and O^T = V^T P^T, so each K/V row is read once for all heads
+//    and little is padded.  (With the heads as the 16 rows, a batch with 4
+//    heads per kv head spent 600 instructions per 16 slots and reached 5.0
+//    TB/s.  The legacy MMA is enough here: a tcgen05 tile would pad the heads
+//    to 128.)
 //  - Each of the four warps takes 16 slots of a tile with its own ring of
 //    cp.async stages and its own softmax state: no block barrier until a
-//    (sequence, head) run ends.
+//    (sequence, head) run ends.  The reference maximum moves only when it
+//    grows by more than 2^8.
 // A run that covers all tiles of its pair writes the output; otherwise its
-// unnormalised fp32 accumulator and (m, l) go to the workspace, and the join
-// kernel combines them in run order (no atomics: results do not depend on
-// timing).  P is rounded to the cache's type for the PV product (relative
+// unnormalised fp32 accumulator and (m, l) go to the workspace, and the run
+// that comes last (a counter per pair, left at zero again) joins the parts in
+// run order: one launch, and results do not depend on timing.  A second kernel
+// adds the weights up where they are wanted.  P is rounded to the cache's type for the PV product (relative
 // error half a step, averaged over the keys); scores, statistics and sums are
 // fp32.
 #pragma once
@@ -36,8 +41,16 @@ namespace bpt {
 constexpr int kDecodeWarps = 4;
 constexpr int kDecodeThreads = kDecodeWarps * 32;
 constexpr int kDecodeTile = 16 * kDecodeWarps;  // slots per tile
-constexpr int kDecodeRows = 16;                 // query heads per MMA
-constexpr int kDecodeCtasPerSm = 2;
+// Blocks per SM and bytes of a block's ring.  Measured, 64 ragged sequences of
+// up to 8192 slots, 8 kv heads of 128 with 4 query heads each: three blocks
+// with two stages per warp 236 us (6.2 TB/s), two with three stages 243, one
+// with six 321.  16 heads at once need 250 registers: two blocks.
+template <int D, int NT>
+struct DecodeShape {
+  static constexpr int CTAS = NT == 2 ? 2 : D == 128 ? 3 : 4;
+  static constexpr int RING = NT == 2 ? 98304 : D == 128 ? 65536 : 32768;
+};
+constexpr int kDecodeMaxCtas = 4;
 constexpr int kDecodeMaxSms = 160;               // the workspace holds partials for so many
 
 struct DecodeParams {
@@ -46,14 +59,17 @@ struct DecodeParams {
   long long q_b, q_h;  // strides, elements
   void* out;
   long long o_b, o_h;
-  uint32_t B, h, g, chunks;  // g = h / h_kv; chunks of 16 heads per kv head
+  uint32_t B, h, g, chunks;  // g = h / h_kv; chunks of `rows` heads per kv head
+  uint32_t rows;             // 8 or 16
   uint32_t window, sinks;    // window 0: every slot
   float scale_log2;
   float* part_o;   // [2 * ctas][16][D]
   float2* part_ml; // [2 * ctas][16]
-  float2* seg_ml;  // [B * h_kv * chunks][16]: (m, l) of pairs done by one CTA
+  float2* seg_ml;  // [B * h_kv * chunks][16]: joined (m, l), where weights are wanted
+  uint32_t* count; // [B * h_kv * chunks]: parts of the pair that are done
   uint32_t ctas;   // grid of the split kernel
-  float* scores;   // nullable [B][h][cap]: s log2(e) of visible slots
+  float* scores;   // nullable [B][h][scores_ld]: s log2(e) of the visible slots, dense
+  long long scores_ld;
   const float* acc;  // nullable [B][h_kv][cap]
   float* acc_out;
 };
@@ -133,23 +149,23 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else
     return pack_bf16x2(lo, hi);
 }
-template <typename T>
-__device__ __forceinline__ T from_float(float v) {
-  if constexpr (std::is_same<T, __half>::value)
-    return __float2half_rn(v);
-  else
-    return __float2bfloat16_rn(v);
+// Transposes an 8 x 8 matrix of 16-bit elements held as one register per lane.
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-template <int D>
+template <int D, int NT>
 struct DecodeCfg {
-  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int ROWS = 8 * NT;          // query heads at once
   static constexpr int SUB = 16 * D * 2;       // 16 rows of K or of V
   static constexpr int STAGE = 2 * SUB;
-  static constexpr int RED_LD = D + 8;         // floats; 8 rows on different banks
+  static constexpr int STAGES = DecodeShape<D, NT>::RING / (kDecodeWarps * STAGE);
+  static constexpr int RED_LD = D + 8;         // floats
   static constexpr int OFF_RED = kDecodeWarps * STAGES * STAGE;
-  static constexpr int OFF_ML = OFF_RED + 16 * RED_LD * 4;
-  static constexpr int SMEM = OFF_ML + kDecodeWarps * 16 * 8;
+  static constexpr int OFF_ML = OFF_RED + ROWS * RED_LD * 4;
+  static constexpr int SMEM = OFF_ML + kDecodeWarps * ROWS * 8;
 };
 
 // Sum over the block of one value per thread.
@@ -171,26 +187,60 @@ __device__ __forceinline__ uint32_t decode_total(const DecodeParams& p, uint32_t
   for (uint32_t b = threadIdx.x; b < p.B; b += blockDim.x) v += decode_seq(p, b, bad).tiles() * per;
   return block_sum_u32(v, scratch);
 }
-// Tiles of the sequences before b.
-__device__ __forceinline__ uint32_t decode_before(const DecodeParams& p, uint32_t b, uint32_t per,
-                                                  uint32_t* scratch) {
-  uint32_t v = 0;
-  bool bad = false;
-  for (uint32_t i = threadIdx.x; i < b; i += blockDim.x) v += decode_seq(p, i, bad).tiles() * per;
-  return block_sum_u32(v, scratch);
+// Joins the parts of a pair that runs lo .. hi hold, by the whole block: the
+// part of run c is its first one, but `second` says whether lo's is its second
+// (the run began in an earlier pair).  Parts come from other SMs: read past L1.
+template <typename T, int D>
+__device__ __noinline__ void decode_join(const DecodeParams& p, uint32_t lo, uint32_t hi,
+                                         uint32_t second, uint32_t heads, long long seg, T* out) {
+  constexpr uint32_t kLanes = D / 4;  // threads of a row, four columns each
+  const uint32_t col = threadIdx.x % kLanes * 4;
+  for (uint32_t row = threadIdx.x / kLanes; row < heads; row += kDecodeThreads / kLanes) {
+    auto at = [&](uint32_t c) { return (2LL * c + (c == lo ? second : 0u)) * 16 + row; };
+    float M = -INFINITY;
+#pragma unroll 4
+    for (uint32_t c = lo; c <= hi; ++c) M = fmaxf(M, __ldcg(p.part_ml + at(c)).x);
+    float L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (uint32_t c = lo; c <= hi; ++c) {
+      const float2 v = __ldcg(p.part_ml + at(c));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(c) * D + col));
+      const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
+      L += v.y * f;
+      a.x += f * x.x;
+      a.y += f * x.y;
+      a.z += f * x.z;
+      a.w += f * x.w;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    if (p.scores != nullptr && col == 0) p.seg_ml[seg * 16 + row] = make_float2(M, L);
+    *reinterpret_cast<uint2*>(out + row * p.o_h + col) =
+        make_uint2(pack2<T>(a.x * inv, a.y * inv), pack2<T>(a.z * inv, a.w * inv));
+  }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
     attn_decode_split_kernel(const DecodeParams p) {
-  using C = DecodeCfg<D>;
+  using C = DecodeCfg<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t scratch[kDecodeWarps];
-  __shared__ uint32_t find_sh[2];
+  __shared__ uint32_t find_sh[2], join_sh[4];
   __shared__ uint32_t vmask[kDecodeWarps][C::STAGES];
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t per = p.c.hkv * p.chunks;
   const uint32_t W = decode_total(p, per, scratch);
+  // sequences without visible slots: zeros
+  for (uint32_t b = blockIdx.x; b < p.B; b += gridDim.x) {
+    bool bad = false;
+    const bool none = decode_seq(p, b, bad).n == 0;
+    if (bad && tid == 0) record_error(p.c.err, kErrIndex, kSiteDecode);
+    if (!none) continue;
+    for (uint32_t x = tid; x < p.h * (D / 8); x += kDecodeThreads)
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + b * p.o_b + (x / (D / 8)) * p.o_h +
+                                x % (D / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
+  }
   const uint32_t G = min(p.ctas, W);  // no run is empty
   if (blockIdx.x >= G) return;        // the whole block
   const uint32_t w0 = run_start(W, G, blockIdx.x), w1 = run_start(W, G, blockIdx.x + 1);
@@ -200,7 +250,6 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
     bool bad = false;
     const uint32_t b = b0 + tid;
     const uint32_t mine = b < p.B ? decode_seq(p, b, bad).tiles() * per : 0;
-    if (bad) record_error(p.c.err, kErrIndex, kSiteDecode);
     uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -226,11 +275,13 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
   // A position in the tile list: sequence, pair in it, tile in the pair.
   struct Cursor {
     uint32_t b, pair, t, tiles;
+    uint32_t base;  // first tile of the sequence in the list
     DecodeSeq s;
   };
   bool bad = false;
   Cursor cc;
   cc.b = find_sh[0];
+  cc.base = find_sh[1];
   cc.s = decode_seq(p, cc.b, bad);
   cc.tiles = cc.s.tiles();
   cc.pair = (w0 - find_sh[1]) / cc.tiles;
@@ -240,6 +291,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
     c.t = 0;
     if (++c.pair < per) return;
     c.pair = 0;
+    c.base += per * c.tiles;
     do {
       ++c.b;
       if (c.b >= p.B) {
@@ -256,7 +308,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
   auto fetch_row = [&](const Cursor& c) -> int {
     const uint32_t u = c.t * kDecodeTile + warp * 16 + (lane & 15);
     if (c.tiles == 0 || u >= c.s.n) return -1;
-    const int row = cache_row(p.c, c.b, c.pair / p.chunks, c.s.slot(u));
+    const int row = cache_row(p.c, c.b, p.chunks == 1 ? c.pair : c.pair / p.chunks, c.s.slot(u));
     bad |= row < 0;
     return row;
   };
@@ -294,37 +346,42 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
     cp_async_commit();
   }
 
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-  float m0, m1, l0, l1;
+  uint32_t qb[NT][D / 16][2];   // Q^T: columns are heads
+  float o[D / 16][NT][4];       // O^T: rows 16 i + r0 (+ 8), heads 8 nt + c0 (+ 1)
+  float m[NT][2], l[NT][2];     // per head; l over this lane's slots
   const uint32_t r0 = lane >> 2, c0 = (lane & 3) * 2;
   bool fresh = true;        // the next tile starts a pair (or the run)
   uint32_t seg_t0 = cc.t;   // first tile of the current pair in this run
   bool first_seg = true;
-  uint32_t stage = 0;
+  uint32_t stage = 0, head0 = 0, heads = 0;
+  float* score = nullptr;   // this lane's first head's row
   for (uint32_t it = 0; it < total; ++it) {
-    const uint32_t kvh = cc.pair / p.chunks, ck = cc.pair - kvh * p.chunks;
-    const uint32_t head0 = kvh * p.g + ck * kDecodeRows;
-    const uint32_t heads = min(static_cast<uint32_t>(kDecodeRows), p.g - ck * kDecodeRows);
     if (fresh) {
       fresh = false;
       seg_t0 = cc.t;
+      const uint32_t kvh = cc.pair / p.chunks, ck = cc.pair - kvh * p.chunks;
+      head0 = kvh * p.g + ck * C::ROWS;
+      heads = min(static_cast<uint32_t>(C::ROWS), p.g - ck * C::ROWS);
       const T* q = static_cast<const T*>(p.q) + cc.b * p.q_b + head0 * p.q_h;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t row = r0 + (x & 1) * 8;
-          qf[k][x] = row < heads ? __ldg(reinterpret_cast<const uint32_t*>(
-                                       q + row * p.q_h + k * 16 + c0 + (x >> 1) * 8))
-                                 : 0u;
-        }
+        for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
+          for (int x = 0; x < 2; ++x)
+            qb[nt][k][x] = 8 * nt + r0 < heads
+                               ? __ldg(reinterpret_cast<const uint32_t*>(
+                                     q + (8 * nt + r0) * p.q_h + k * 16 + c0 + 8 * x))
+                               : 0u;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
-      m0 = m1 = -INFINITY;
-      l0 = l1 = 0.f;
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[i][nt][x] = 0.f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+      }
+      if (p.scores != nullptr)
+        score = p.scores + (static_cast<long long>(cc.b) * p.h + head0 + c0) * p.scores_ld;
     }
     cp_async_wait<C::STAGES - 2>();
     __syncwarp();
@@ -341,167 +398,180 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
     }
     const uint32_t kb = ring + stage * C::STAGE, vb = kb + C::SUB;
     const uint32_t valid = vmask[warp][stage];
-    // S = Q K^T: 16 heads x 16 slots
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    // S^T = K Q^T: 16 slots x heads, even and odd steps apart (shorter chains)
+    float s[NT][4] = {}, s2[NT][4] = {};
     {
-      const uint32_t key = ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
+      const uint32_t key = (((lane >> 3) & 1) << 3) + (lane & 7), kc = lane >> 4;
       const uint32_t a = kb + key * (D * 2);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t r[4];
         ldsm_x4(r, a + (((2 * k + kc) ^ (key & 7)) << 4));
-        mma_16816<T>(s[0], qf[k], r[0], r[1]);
-        mma_16816<T>(s[1], qf[k], r[2], r[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_16816<T>((k & 1) ? s2[nt] : s[nt], r, qb[nt][k][0], qb[nt][k][1]);
       }
     }
+    const bool part_tile = valid != 0xFFFFu;
+    bool grow = false;
+    float mx[NT][2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        s[n][x] = ((valid >> (n * 8 + c0 + (x & 1))) & 1u) ? s[n][x] * p.scale_log2 : -INFINITY;
-    if (p.scores != nullptr) {
+      for (int x = 0; x < 4; ++x) s[nt][x] = (s[nt][x] + s2[nt][x]) * p.scale_log2;
+      if (part_tile) {
+        if (!((valid >> r0) & 1u)) s[nt][0] = s[nt][1] = -INFINITY;
+        if (!((valid >> (r0 + 8)) & 1u)) s[nt][2] = s[nt][3] = -INFINITY;
+      }
+      if (p.scores != nullptr) {
+        const uint32_t u = cc.t * kDecodeTile + warp * 16 + r0;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int x = 0; x < 4; ++x)
+          if (8 * nt + c0 + (x & 1) < heads && u + 8 * (x >> 1) < cc.s.n)
+            score[(8 * nt + (x & 1)) * p.scores_ld + u + 8 * (x >> 1)] = s[nt][x];
+      }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t row = r0 + (x >> 1) * 8;
-          const uint32_t u = cc.t * kDecodeTile + warp * 16 + n * 8 + c0 + (x & 1);
-          if (row < heads && u < cc.s.n)
-            p.scores[(static_cast<long long>(cc.b) * p.h + head0 + row) * p.c.cap + cc.s.slot(u)] =
-                s[n][x];
+      for (int j = 0; j < 2; ++j) {
+        float v = fmaxf(s[nt][j], s[nt][2 + j]);
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        mx[nt][j] = v;
+        grow |= v > m[nt][j] + 8.f;  // (-inf + 8 = -inf: the first visible slot counts)
+      }
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float n = fmaxf(m[nt][j], mx[nt][j]);
+          const float a = m[nt][j] == -INFINITY ? 0.f : ex2_approx(m[nt][j] - n);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[i][nt][j] *= a;
+            o[i][nt][2 + j] *= a;
+          }
+          l[nt][j] *= a;
+          m[nt][j] = n;
         }
     }
-    float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-    float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-    const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-    if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-      const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0);
-      const float a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
+    uint32_t pb[NT][2];
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= a0;
-        o[n][1] *= a0;
-        o[n][2] *= a1;
-        o[n][3] *= a1;
-      }
-      l0 *= a0;
-      l1 *= a1;
-      m0 = n0;
-      m1 = n1;
+    for (int nt = 0; nt < NT; ++nt) {
+      // a head that has seen nothing keeps reference 0: exp2(-inf) = 0
+      const float f0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+      const float f1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+      s[nt][0] = ex2_approx(s[nt][0] - f0);
+      s[nt][1] = ex2_approx(s[nt][1] - f1);
+      s[nt][2] = ex2_approx(s[nt][2] - f0);
+      s[nt][3] = ex2_approx(s[nt][3] - f1);
+      l[nt][0] += s[nt][0] + s[nt][2];
+      l[nt][1] += s[nt][1] + s[nt][3];
+      pb[nt][0] = movm_t(pack2<T>(s[nt][0], s[nt][1]));
+      pb[nt][1] = movm_t(pack2<T>(s[nt][2], s[nt][3]));
     }
-    // a row that has seen nothing keeps reference 0: exp2(-inf) = 0
-    const float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      s[n][0] = ex2_approx(s[n][0] - f0);
-      s[n][1] = ex2_approx(s[n][1] - f0);
-      s[n][2] = ex2_approx(s[n][2] - f1);
-      s[n][3] = ex2_approx(s[n][3] - f1);
-      l0 += s[n][0] + s[n][1];
-      l1 += s[n][2] + s[n][3];
-    }
-    const uint32_t pf[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
-                            pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
     {
-      const uint32_t key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+      const uint32_t key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
       const uint32_t a = vb + key * (D * 2);
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
+      for (int i = 0; i < D / 16; ++i) {
         uint32_t r[4];
-        ldsm_x4_t(r, a + (((2 * n + half) ^ (key & 7)) << 4));
-        mma_16816<T>(o[2 * n], pf, r[0], r[1]);
-        mma_16816<T>(o[2 * n + 1], pf, r[2], r[3]);
+        ldsm_x4_t(r, a + (((2 * i + half) ^ (key & 7)) << 4));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16816<T>(o[i][nt], r, pb[nt][0], pb[nt][1]);
       }
     }
     if (++stage == C::STAGES) stage = 0;
 
     const bool pair_end = cc.t + 1 == cc.tiles;
     if (pair_end || it + 1 == total) {
-      // join the four warps: reference maximum, then the accumulators
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      // join the four warps: reference maximum, then the accumulators in order
       float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
       float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
-      if ((lane & 3) == 0) {
-        ml[warp * 16 + r0] = make_float2(m0, l0);
-        ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
-      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v = l[nt][j];
+          v += __shfl_xor_sync(0xffffffffu, v, 4);
+          v += __shfl_xor_sync(0xffffffffu, v, 8);
+          v += __shfl_xor_sync(0xffffffffu, v, 16);
+          if (r0 == 0) ml[warp * C::ROWS + 8 * nt + c0 + j] = make_float2(m[nt][j], v);
+        }
       __syncthreads();
-      float M[2], L[2], f[2];
+      float f[NT][2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t row = r0 + x * 8;
-        M[x] = -INFINITY;
-        for (int w = 0; w < kDecodeWarps; ++w) M[x] = fmaxf(M[x], ml[w * 16 + row].x);
-        L[x] = 0.f;
-        for (int w = 0; w < kDecodeWarps; ++w) {
-          const float2 v = ml[w * 16 + row];
-          L[x] += v.x == -INFINITY ? 0.f : v.y * ex2_approx(v.x - M[x]);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float M = -INFINITY;
+          for (int w = 0; w < kDecodeWarps; ++w)
+            M = fmaxf(M, ml[w * C::ROWS + 8 * nt + c0 + j].x);
+          f[nt][j] = m[nt][j] == -INFINITY ? 0.f : ex2_approx(m[nt][j] - M);
         }
-        const float mine = x == 0 ? m0 : m1;
-        f[x] = mine == -INFINITY ? 0.f : ex2_approx(mine - M[x]);
-      }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= f[0];
-        o[n][1] *= f[0];
-        o[n][2] *= f[1];
-        o[n][3] *= f[1];
-      }
-      auto rows_do = [&](auto f) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t row = r0 + x * 8;
-          if (row >= heads) continue;
-          float* d = red + row * C::RED_LD + c0;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            f(reinterpret_cast<float2*>(d + n * 8), o[n][2 * x], o[n][2 * x + 1]);
-        }
-      };
-      // warp 0 adds the others' accumulators in warp order, one buffer
 #pragma unroll 1
-      for (uint32_t w = 1; w < kDecodeWarps; ++w) {
-        if (warp == w)
-          rows_do([](float2* d, float& a, float& b) { *d = make_float2(a, b); });
-        __syncthreads();
-        if (warp == 0)
-          rows_do([](float2* d, float& a, float& b) {
-            const float2 v = *d;
-            a += v.x;
-            b += v.y;
-          });
+      for (uint32_t w = 0; w < kDecodeWarps; ++w) {
+        if (warp == w) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t row = 8 * nt + c0 + (x & 1);
+                if (row >= heads) continue;
+                float* d = red + row * C::RED_LD + 16 * i + r0 + 8 * (x >> 1);
+                const float v = o[i][nt][x] * f[nt][x & 1];
+                *d = w == 0 ? v : *d + v;
+              }
+        }
         __syncthreads();
       }
-      if (warp == 0) {
-        const bool whole = seg_t0 == 0 && pair_end;
-        const uint32_t ps = blockIdx.x * 2 + (first_seg ? 0 : 1);
-        const long long seg = static_cast<long long>(cc.b) * per + cc.pair;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t row = r0 + x * 8;
-          if (row >= heads) continue;
-          if ((lane & 3) == 0)
-            (whole ? p.seg_ml + seg * 16 : p.part_ml + ps * 16LL)[row] = make_float2(M[x], L[x]);
-          if (whole) {
-            const float inv = L[x] > 0.f ? 1.f / L[x] : 0.f;
-            T* dst = static_cast<T*>(p.out) + cc.b * p.o_b + (head0 + row) * p.o_h + c0;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-              *reinterpret_cast<uint32_t*>(dst + n * 8) =
-                  pack2<T>(o[n][2 * x] * inv, o[n][2 * x + 1] * inv);
-          } else {
-            float* dst = p.part_o + (ps * 16LL + row) * D + c0;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-              *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
-          }
+      const bool whole = seg_t0 == 0 && pair_end;
+      const long long seg = static_cast<long long>(cc.b) * per + cc.pair;
+      const uint32_t ps = blockIdx.x * 2 + (first_seg ? 0 : 1);
+      constexpr uint32_t kLanes = D / 4;  // threads of a row, four columns each
+      const uint32_t col = tid % kLanes * 4;
+      for (uint32_t row = tid / kLanes; row < heads; row += kDecodeThreads / kLanes) {
+        const float4 v = *reinterpret_cast<const float4*>(red + row * C::RED_LD + col);
+        float M = -INFINITY, L = 0.f;
+        for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, ml[w * C::ROWS + row].x);
+        for (int w = 0; w < kDecodeWarps; ++w) {
+          const float2 x = ml[w * C::ROWS + row];
+          L += x.x == -INFINITY ? 0.f : x.y * ex2_approx(x.x - M);
+        }
+        if (!whole) {
+          if (col == 0) p.part_ml[ps * 16LL + row] = make_float2(M, L);
+          *reinterpret_cast<float4*>(p.part_o + (ps * 16LL + row) * D + col) = v;
+          continue;
+        }
+        if (p.scores != nullptr && col == 0) p.seg_ml[seg * 16 + row] = make_float2(M, L);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + cc.b * p.o_b + (head0 + row) * p.o_h +
+                                  col) =
+            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+      }
+      if (!whole) {
+        __threadfence();  // this part is visible to everyone before it is counted
+        __syncthreads();
+        if (tid == 0) {
+          const uint32_t s0 = cc.base + cc.pair * cc.tiles;
+          const uint32_t lo = run_of(W, G, s0), hi = run_of(W, G, s0 + cc.tiles - 1);
+          const bool last = atomicAdd(p.count + seg, 1u) == hi - lo;
+          if (last) p.count[seg] = 0;
+          join_sh[0] = last ? 1u : 0u;
+          join_sh[1] = lo;
+          join_sh[2] = hi;
+          join_sh[3] = run_start(W, G, lo) < s0 ? 1u : 0u;  // lo's second part
+        }
+      }
+      if (!whole) {
+        __syncthreads();
+        if (join_sh[0]) {
+          __threadfence();
+          decode_join<T, D>(p, join_sh[1], join_sh[2], join_sh[3], heads, seg,
+                            static_cast<T*>(p.out) + cc.b * p.o_b + head0 * p.o_h);
         }
       }
       __syncthreads();  // ml is free again
@@ -514,107 +584,51 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
   if (bad) record_error(p.c.err, kErrIndex, kSiteDecode);
 }
 
-constexpr int kJoinThreads = 256;
-constexpr int kJoinSlots = 2048;  // slots of accumulated weight per block
+constexpr int kWeightThreads = 256;
+constexpr int kWeightSlots = 2048;  // slots per block
 
-// Where pair `seg` of sequence b lies: its tiles [s0, s1) and the runs lo..hi
-// that hold it.  Partial of run c: its first pair unless the run began before.
-struct DecodeSpan {
-  uint32_t s0, s1, lo, hi, W, G;
-  __device__ __forceinline__ uint32_t part(uint32_t c) const {
-    return 2 * c + (run_start(W, G, c) < s0 ? 1 : 0);
-  }
-};
-__device__ __forceinline__ DecodeSpan decode_span(const DecodeParams& p, uint32_t b, uint32_t pair,
-                                                  uint32_t per, uint32_t tiles, uint32_t W,
-                                                  uint32_t before) {
-  DecodeSpan d;
-  d.W = W;
-  d.G = min(p.ctas, W);
-  d.s0 = before + pair * tiles;
-  d.s1 = d.s0 + tiles;
-  d.lo = run_of(W, d.G, d.s0);
-  d.hi = run_of(W, d.G, d.s1 - 1);
-  return d;
-}
-
-// Grid (B * h_kv, 1 + slot blocks).  y = 0: joins the partial results of the
-// pair's heads, one warp per head, and writes zeros for an empty sequence.
-// y > 0: acc_out = acc + the weight each slot received, from the saved scores
-// and the joined (m, l).
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const DecodeParams p) {
-  __shared__ uint32_t scratch[kJoinThreads / 32];
+// Grid (slot blocks, h_kv, B): acc_out = acc + the weight each slot received,
+// from the saved scores and the joined (m, l).
+__global__ void __launch_bounds__(kWeightThreads) attn_decode_weights_kernel(const DecodeParams p) {
   __shared__ float2 ml_sh[256];
-  const uint32_t per = p.c.hkv * p.chunks;
-  const uint32_t b = blockIdx.x / p.c.hkv, kvh = blockIdx.x - b * p.c.hkv;
-  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t b = blockIdx.z, kvh = blockIdx.y, tid = threadIdx.x;
   bool bad = false;
   const DecodeSeq sq = decode_seq(p, b, bad);
-  if (bad && tid == 0) record_error(p.c.err, kErrIndex, kSiteDecode);
-  const uint32_t tiles = sq.tiles();
-  if (blockIdx.y > 0 && (blockIdx.y - 1) * kJoinSlots >= sq.len) return;
-  const uint32_t W = decode_total(p, per, scratch);
-  const uint32_t before = decode_before(p, b, per, scratch);
-  if (blockIdx.y == 0) {
-    for (uint32_t r = warp; r < p.g; r += kJoinThreads / 32) {
-      const uint32_t ck = r / kDecodeRows, row = r - ck * kDecodeRows;
-      T* dst = static_cast<T*>(p.out) + b * p.o_b + (kvh * p.g + r) * p.o_h;
-      if (tiles == 0) {
-        for (uint32_t c = lane; c < D; c += 32) dst[c] = from_float<T>(0.f);
-        continue;
-      }
-      const DecodeSpan sp = decode_span(p, b, kvh * p.chunks + ck, per, tiles, W, before);
-      if (sp.lo == sp.hi) continue;  // written by its run
-      float M = -INFINITY;
-      for (uint32_t c = sp.lo; c <= sp.hi; ++c)
-        M = fmaxf(M, p.part_ml[sp.part(c) * 16LL + row].x);
-      float L = 0.f;
-      float a[D / 32] = {};
-      for (uint32_t c = sp.lo; c <= sp.hi; ++c) {
-        const long long pr = sp.part(c) * 16LL + row;
-        const float2 v = p.part_ml[pr];
-        const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
-        L += v.y * f;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) a[k] += f * p.part_o[pr * D + k * 32 + lane];
-      }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) dst[k * 32 + lane] = from_float<T>(a[k] * inv);
-    }
-    return;
-  }
-  // accumulated weights: (m, 1 / l) of the pair's heads first
-  for (uint32_t r = tid; r < p.g; r += kJoinThreads) {
-    if (tiles == 0) break;
-    const uint32_t ck = r / kDecodeRows, row = r - ck * kDecodeRows;
-    const uint32_t pair = kvh * p.chunks + ck;
-    const DecodeSpan sp = decode_span(p, b, pair, per, tiles, W, before);
-    float2 v;
-    if (sp.lo == sp.hi) {
-      v = p.seg_ml[(static_cast<long long>(b) * per + pair) * 16 + row];
-    } else {
-      v = make_float2(-INFINITY, 0.f);
-      for (uint32_t c = sp.lo; c <= sp.hi; ++c)
-        v.x = fmaxf(v.x, p.part_ml[sp.part(c) * 16LL + row].x);
-      for (uint32_t c = sp.lo; c <= sp.hi; ++c) {
-        const float2 y = p.part_ml[sp.part(c) * 16LL + row];
-        v.y += y.x == -INFINITY ? 0.f : y.y * ex2_approx(y.x - v.x);
-      }
-    }
+  if (blockIdx.x * kWeightSlots >= sq.len) return;
+  // (m, 1 / l) of the pair's heads
+  for (uint32_t r = tid; r < p.g; r += kWeightThreads) {
+    const uint32_t ck = r / p.rows, row = r - ck * p.rows;
+    const long long seg = (static_cast<long long>(b) * p.c.hkv + kvh) * p.chunks + ck;
+    const float2 v = p.seg_ml[seg * 16 + row];
     ml_sh[r] = make_float2(v.x == -INFINITY ? 0.f : v.x, v.y > 0.f ? 1.f / v.y : 0.f);
   }
   __syncthreads();
   const long long a0 = (static_cast<long long>(b) * p.c.hkv + kvh) * p.c.cap;
-  const float* sc = p.scores + (static_cast<long long>(b) * p.h + kvh * p.g) * p.c.cap;
-  const uint32_t s_end = min(sq.len, blockIdx.y * kJoinSlots);
-  for (uint32_t s = (blockIdx.y - 1) * kJoinSlots + tid; s < s_end; s += kJoinThreads) {
-    float w = 0.f;
-    if (s >= sq.lo || s < sq.ns)
-      for (uint32_t r = 0; r < p.g; ++r)
-        w += ex2_approx(sc[static_cast<long long>(r) * p.c.cap + s] - ml_sh[r].x) * ml_sh[r].y;
-    p.acc_out[a0 + s] = p.acc[a0 + s] + w;
+  const float* sc = p.scores + (static_cast<long long>(b) * p.h + kvh * p.g) * p.scores_ld;
+  const uint32_t first = blockIdx.x * kWeightSlots + tid;
+  // four slots at a time, their loads independent
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWeightSlots / kWeightThreads; i += 4) {
+    float w[4] = {}, old[4];
+    const float* at[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t s = first + (i + x) * kWeightThreads;
+      const bool seen = s < sq.len && (s >= sq.lo || s < sq.ns);
+      at[x] = seen ? sc + (s < sq.ns ? s : sq.ns + (s - sq.lo)) : nullptr;
+      old[x] = s < sq.len ? p.acc[a0 + s] : 0.f;
+    }
+    for (uint32_t r = 0; r < p.g; ++r) {
+      const float2 ml = ml_sh[r];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (at[x] != nullptr) w[x] += ex2_approx(at[x][r * p.scores_ld] - ml.x) * ml.y;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t s = first + (i + x) * kWeightThreads;
+      if (s < sq.len) p.acc_out[a0 + s] = old[x] + w[x];
+    }
   }
 }
 

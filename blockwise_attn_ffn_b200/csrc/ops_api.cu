@@ -82,10 +82,16 @@ bpt_status ops_device(int* sms) {
     d.sms = n;
     using bf = __nv_bfloat16;
     if (d.ok &&
-        (smem_fails(bpt::attn_decode_split_kernel<bf, 64>, bpt::DecodeCfg<64>::SMEM) ||
-         smem_fails(bpt::attn_decode_split_kernel<bf, 128>, bpt::DecodeCfg<128>::SMEM) ||
-         smem_fails(bpt::attn_decode_split_kernel<__half, 64>, bpt::DecodeCfg<64>::SMEM) ||
-         smem_fails(bpt::attn_decode_split_kernel<__half, 128>, bpt::DecodeCfg<128>::SMEM) ||
+        (smem_fails(bpt::cache_evict_select_kernel<false>, bpt::kEvictSmem) ||
+         smem_fails(bpt::cache_evict_select_kernel<true>, bpt::kEvictSmem) ||
+         smem_fails(bpt::attn_decode_split_kernel<bf, 64, 1>, bpt::DecodeCfg<64, 1>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<bf, 64, 2>, bpt::DecodeCfg<64, 2>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<bf, 128, 1>, bpt::DecodeCfg<128, 1>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<bf, 128, 2>, bpt::DecodeCfg<128, 2>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<__half, 64, 1>, bpt::DecodeCfg<64, 1>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<__half, 64, 2>, bpt::DecodeCfg<64, 2>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<__half, 128, 1>, bpt::DecodeCfg<128, 1>::SMEM) ||
+         smem_fails(bpt::attn_decode_split_kernel<__half, 128, 2>, bpt::DecodeCfg<128, 2>::SMEM) ||
          smem_fails(bpt::attn_window_tc_kernel<bf, 64>, bpt::WindowCfg<64>::SMEM) ||
          smem_fails(bpt::attn_window_tc_kernel<bf, 128>, bpt::WindowCfg<128>::SMEM) ||
          smem_fails(bpt::attn_window_tc_kernel<__half, 64>, bpt::WindowCfg<64>::SMEM) ||
@@ -149,6 +155,14 @@ bpt::CacheView view_of(const bpt_cache* c, void* ws) {
   v.ps = uint32_t(c->page_size);
   v.max_pages = uint32_t(c->max_pages);
   v.cap = uint32_t(c->max_pages * c->page_size);
+  // ps_mul = ceil(2^(31 + l) / ps) with 2^(l-1) < ps <= 2^l: the product's
+  // error stays below 2^-l for 31-bit slots, so the quotient is exact
+  if (v.ps > 1) {
+    int l = 0;
+    while ((uint64_t(1) << l) < v.ps) ++l;
+    v.ps_mul = uint32_t(((uint64_t(1) << (31 + l)) + v.ps - 1) / v.ps);
+    v.ps_shift = uint32_t(l - 1);
+  }
   v.err = static_cast<uint32_t*>(ws);
   return v;
 }
@@ -167,39 +181,48 @@ CacheLayout cache_layout(const bpt_cache* c) {
 }
 
 struct DecodeLayout {
-  size_t off_o, off_ml, off_seg, off_scores, total;
-  int64_t chunks;
+  size_t off_count, off_o, off_ml, off_seg, off_scores, total;
+  int64_t chunks, rows;
 };
+// Row length of the saved scores (dense over the visible slots), even.
+int64_t scores_ld(const bpt_cache* c) { return (c->max_pages * c->page_size + 1) / 2 * 2; }
 bpt_status decode_layout(const bpt_cache* c, int64_t heads, int with_acc, DecodeLayout* l) {
   if (heads <= 0 || heads % c->kv_heads != 0) return BPT_ERR_INVALID_ARG;
   const int64_t g = heads / c->kv_heads;
   if (g > 256) return BPT_ERR_UNSUPPORTED;
-  l->chunks = (g + bpt::kDecodeRows - 1) / bpt::kDecodeRows;
+  // query heads that go through one pass over the keys: 8 or 16
+  l->rows = g <= 8 ? 8 : 16;
+  l->chunks = (g + l->rows - 1) / l->rows;
   const int64_t tiles = (c->max_pages * c->page_size + bpt::kDecodeTile - 1) / bpt::kDecodeTile;
   const int64_t pairs = c->batch * c->kv_heads * l->chunks;
   if (pairs >= (int64_t(1) << 31) || (pairs > 0 && tiles >= (int64_t(1) << 31) / pairs) ||
       c->batch * c->kv_heads >= (int64_t(1) << 31))
     return BPT_ERR_UNSUPPORTED;
-  const size_t parts = size_t(2 * bpt::kDecodeCtasPerSm * bpt::kDecodeMaxSms) * 16;
-  l->off_o = kOpsHeader;
+  const size_t parts = size_t(2 * bpt::kDecodeMaxCtas * bpt::kDecodeMaxSms) * 16;
+  l->off_count = kOpsHeader;
+  l->off_o = align_to(l->off_count + size_t(pairs) * 4, 256);
   l->off_ml = align_to(l->off_o + parts * size_t(c->d_k) * 4, 256);
   l->off_seg = align_to(l->off_ml + parts * 8, 256);
   l->off_scores = align_to(l->off_seg + size_t(pairs) * 16 * 8, 256);
   l->total = l->off_scores;
   if (with_acc)
     l->total = align_to(l->off_scores + size_t(c->batch * heads) *
-                                            size_t(c->max_pages * c->page_size) * 4, 256);
+                                            size_t(scores_ld(c)) * 4, 256);
   return BPT_OK;
 }
 
 template <typename T, int D>
 cudaError_t launch_decode(const bpt::DecodeParams& p, unsigned slot_blocks, cudaStream_t s) {
-  bpt::attn_decode_split_kernel<T, D>
-      <<<p.ctas, bpt::kDecodeThreads, bpt::DecodeCfg<D>::SMEM, s>>>(p);
+  if (p.rows == 8)
+    bpt::attn_decode_split_kernel<T, D, 1>
+        <<<p.ctas, bpt::kDecodeThreads, bpt::DecodeCfg<D, 1>::SMEM, s>>>(p);
+  else
+    bpt::attn_decode_split_kernel<T, D, 2>
+        <<<p.ctas, bpt::kDecodeThreads, bpt::DecodeCfg<D, 2>::SMEM, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  bpt::attn_decode_join_kernel<T, D>
-      <<<dim3(p.B * p.c.hkv, 1 + slot_blocks), bpt::kJoinThreads, 0, s>>>(p);
+  if (slot_blocks == 0) return cudaSuccess;
+  bpt::attn_decode_weights_kernel<<<dim3(slot_blocks, p.c.hkv, p.B), bpt::kWeightThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -486,13 +509,40 @@ bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recen
   p.count = reinterpret_cast<int*>(ws + l.off_count);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned hkv = unsigned(cache->kv_heads);
-  bpt::cache_evict_select_kernel<<<dim3(hkv, unsigned(B)), bpt::kEvictThreads, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return BPT_ERR_CUDA;
+  // Blocks per pair: about 4096 slots each (four per thread), at most a
+  // portable cluster.  Up to there one block holds a pair and moves its rows
+  // itself: eight caches of 1300 slots, 12 heads, take 16.5 us with a launch of
+  // its own for the moves, which is only needed where new_lens is lens.
+  unsigned C = 1;
+  while (C < bpt::kEvictMaxCluster && p.c.cap > C * 4096u &&
+         B * int64_t(hkv) * int64_t(2 * C) <= 2 * sms)
+    C *= 2;
+  const bool fused = C == 1 && new_lens != cache->lens;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(hkv * C, unsigned(B));
+  cfg.blockDim = dim3(bpt::kEvictThreads);
+  cfg.dynamicSmemBytes = bpt::kEvictSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  if ((fused ? cudaLaunchKernelEx(&cfg, bpt::cache_evict_select_kernel<true>, p, uint32_t(C))
+             : cudaLaunchKernelEx(&cfg, bpt::cache_evict_select_kernel<false>, p, uint32_t(C))) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return BPT_ERR_CUDA;
+  }
+  if (fused) return BPT_OK;
   // at most min(budget, capacity / 2) rows of a pair move; enough blocks to
   // fill the device, at least one step each
   const int64_t moves = std::min<int64_t>(p.budget, int64_t(p.c.cap) / 2);
-  const int64_t steps = (moves + bpt::kMoveRows - 1) / bpt::kMoveRows;
-  const int64_t fill = std::max<int64_t>(1, int64_t(sms) * 32 / (B * int64_t(hkv)));
+  const int64_t per = bpt::kMoveThreads / int64_t(p.row16);
+  const int64_t steps = (moves + per - 1) / per;
+  const int64_t fill = std::max<int64_t>(1, int64_t(sms) * 16 / (B * int64_t(hkv)));
   const unsigned gx = unsigned(std::max<int64_t>(1, std::min(steps, fill)));
   bpt::cache_evict_move_kernel<<<dim3(gx, hkv, unsigned(B)), bpt::kMoveThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
@@ -564,19 +614,24 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
   p.h = uint32_t(heads);
   p.g = uint32_t(heads / cache->kv_heads);
   p.chunks = uint32_t(l.chunks);
+  p.rows = uint32_t(l.rows);
+  p.scores_ld = scores_ld(cache);
   p.window = clamp_u31(window);
   p.sinks = clamp_u31(sinks);
   p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
+  p.count = reinterpret_cast<uint32_t*>(ws + l.off_count);
   p.part_o = reinterpret_cast<float*>(ws + l.off_o);
   p.part_ml = reinterpret_cast<float2*>(ws + l.off_ml);
   p.seg_ml = reinterpret_cast<float2*>(ws + l.off_seg);
-  p.ctas = uint32_t(bpt::kDecodeCtasPerSm * std::min(sms, bpt::kDecodeMaxSms));
+  const int per_sm = l.rows == 16 ? bpt::DecodeShape<128, 2>::CTAS
+                     : dk == 128  ? bpt::DecodeShape<128, 1>::CTAS
+                                  : bpt::DecodeShape<64, 1>::CTAS;
+  p.ctas = uint32_t(per_sm * std::min(sms, bpt::kDecodeMaxSms));
   p.scores = acc != nullptr ? reinterpret_cast<float*>(ws + l.off_scores) : nullptr;
   p.acc = acc;
   p.acc_out = acc_out;
   const unsigned slot_blocks =
-      acc != nullptr ? unsigned((p.c.cap + bpt::kJoinSlots - 1) / bpt::kJoinSlots) : 0u;
-  if (slot_blocks > 65000) return BPT_ERR_UNSUPPORTED;
+      acc != nullptr ? unsigned((p.c.cap + bpt::kWeightSlots - 1) / bpt::kWeightSlots) : 0u;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cache->dtype == BPT_BF16)

@@ -618,7 +618,9 @@ bpt_status bpt_layer_forward_static(const void* x, const void* ln1, const void* 
  * Workspaces of these operators: 256-byte aligned, the FIRST 256 BYTES ZEROED
  * BY THE CALLER ONCE before the first use (the error word lives there; it
  * keeps the first fault until bpt_read_device_error returns and clears it).
- * The rest needs no initialisation.  Calls that may overlap on the GPU
+ * bpt_attn_decode's workspace is zeroed whole, once: it holds counters that
+ * every call leaves at zero.  The rest needs no initialisation.  Calls that may
+ * overlap on the GPU
  * (different streams, graphs launched side by side) need a workspace each.
  * All calls may be captured into a CUDA graph.
  */

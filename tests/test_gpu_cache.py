@@ -306,6 +306,9 @@ def check_evicted(pool, before, acc, pos, seen, budget, recent, sinks, got, tail
     ([5000, 4100], 2, 128, 64, 1000, 0, 0, "bf16", True),
     ([600], 2, 64, 16, 500, 600, 0, "f16", False),            # more protected than the budget
     ([40, 20], 2, 64, 16, 400, 5, 1, "bf16", False),          # nothing to do
+    ([9001, 7000], 1, 64, 48, 3000, 100, 4, "f16", False),    # two, four and eight blocks per pair
+    ([15000, 5], 1, 64, 64, 7600, 0, 0, "bf16", True),
+    ([140001], 1, 64, 128, 20011, 500, 4, "f16", True),       # keys past the shared memory
 ], ids=str)
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_keeps_what_the_definition_keeps(lens, hkv, dk, ps, budget, recent, sinks, dt, ties,
