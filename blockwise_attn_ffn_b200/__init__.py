@@ -12,7 +12,10 @@ from ._lib import (  # noqa: F401
     BptError, Cache, Options, Rows, Window, bpt_attn_decode, bpt_attn_decode_workspace_size,
     bpt_attn_window_backward, bpt_attn_window_backward_workspace_size, bpt_attn_window_forward,
     bpt_attn_window_workspace_size, bpt_cache_append,
-    bpt_cache_evict, bpt_cache_workspace_size, bpt_layer_backward, bpt_layer_backward_keep_o, bpt_layer_backward_opt,
+    bpt_cache_evict, bpt_cache_workspace_size, bpt_layer_backward, bpt_layer_backward_window,
+    bpt_layer_backward_window_workspace_size, bpt_layer_decode, bpt_layer_decode_prepare,
+    bpt_layer_decode_workspace_size, bpt_layer_forward_window,
+    bpt_layer_forward_window_workspace_size, bpt_layer_backward_keep_o, bpt_layer_backward_opt,
     bpt_layer_backward_workspace_size, bpt_layer_backward_workspace_size_opt,
     bpt_layer_forward, bpt_layer_forward_bsfa, bpt_layer_forward_bsfa_opt, bpt_layer_forward_opt,
     bpt_layer_forward_static, bpt_layer_forward_train, bpt_layer_forward_train_keep_o,
@@ -32,5 +35,6 @@ from .cache import (  # noqa: F401
 )
 from .layer import (  # noqa: F401
     GRAD_SHAPES, PARAM_NAMES, layer_backward, layer_forward, layer_forward_bsfa,
-    layer_forward_train, to_device, workspace_for,
+    layer_backward_window, layer_decode, layer_decode_workspace, layer_forward_train,
+    layer_forward_window, to_device, workspace_for,
 )

@@ -40,6 +40,9 @@ EXPORTED = [
     "bpt_attn_decode_workspace_size", "bpt_attn_decode",
     "bpt_attn_window_workspace_size", "bpt_attn_window_forward",
     "bpt_attn_window_backward_workspace_size", "bpt_attn_window_backward",
+    "bpt_layer_forward_window_workspace_size", "bpt_layer_forward_window",
+    "bpt_layer_backward_window_workspace_size", "bpt_layer_backward_window",
+    "bpt_layer_decode_workspace_size", "bpt_layer_decode_prepare", "bpt_layer_decode",
 ]
 
 
@@ -192,6 +195,20 @@ def load() -> ctypes.CDLL:
     lib.bpt_attn_window_backward_workspace_size.argtypes = [pw, pz]
     lib.bpt_attn_window_backward.argtypes = [pw, pr, pr, pr, pr, vp, pr, vp, pr, pr, pr, vp, sz,
                                              vp]
+    lib.bpt_layer_forward_window_workspace_size.argtypes = [i64] * 5 + [i32, pz]
+    lib.bpt_layer_forward_window.argtypes = ([vp] * 11 + [i64] * 5 + [i32, i64, i64] + [vp] * 4 +
+                                             [pc] + [vp] * 5 + [sz, vp])
+    lib.bpt_layer_backward_window_workspace_size.argtypes = [i64] * 5 + [i32, i64, i64, pz]
+    lib.bpt_layer_backward_window.argtypes = ([vp] * 14 + [i64] * 5 + [i32, i64, i64] +
+                                              [vp] * 13 + [sz, vp])
+    lib.bpt_layer_decode_workspace_size.argtypes = [pc, i64, i64, i32, pz]
+    lib.bpt_layer_decode_prepare.argtypes = [vp] * 6 + [pc, i64, i64, i32, vp, sz, vp]
+    lib.bpt_layer_decode.argtypes = [vp] * 5 + [pc] + [i64] * 4 + [vp] * 6 + [sz, vp]
+    for fn in (lib.bpt_layer_forward_window_workspace_size, lib.bpt_layer_forward_window,
+               lib.bpt_layer_backward_window_workspace_size, lib.bpt_layer_backward_window,
+               lib.bpt_layer_decode_workspace_size, lib.bpt_layer_decode_prepare,
+               lib.bpt_layer_decode):
+        fn.restype = i32
     for fn in (lib.bpt_cache_workspace_size, lib.bpt_cache_append, lib.bpt_cache_evict,
                lib.bpt_attn_decode_workspace_size, lib.bpt_attn_decode,
                lib.bpt_attn_window_workspace_size, lib.bpt_attn_window_forward,
@@ -480,3 +497,63 @@ def bpt_attn_window_backward(window, q, k, v, o, stats, d_o, lens, dq, dk, dv, w
     """Pointer-level call (lens may be None); returns the status."""
     return load().bpt_attn_window_backward(window, q, k, v, o, stats, d_o, lens, dq, dk, dv,
                                            workspace, workspace_bytes, stream)
+
+
+# --------------------------- the layer with a window and with a cache --
+def bpt_layer_forward_window_workspace_size(B, N, d, h, d_ff, dtype) -> Tuple[int, int]:
+    """Returns (status, bytes)."""
+    out = ctypes.c_size_t(0)
+    st = load().bpt_layer_forward_window_workspace_size(B, N, d, h, d_ff, dtype, ctypes.byref(out))
+    return st, out.value
+
+
+def bpt_layer_forward_window(x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, B, N, d, h, d_ff,
+                             dtype, window, sinks, lens, out, stats, o, cache, new_lens, acc, pos,
+                             seen, workspace, workspace_bytes, stream) -> int:
+    """Pointer-level call (lens, stats, o, cache and its state may be None)."""
+    return load().bpt_layer_forward_window(x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, B,
+                                           N, d, h, d_ff, dtype, window, sinks, lens, out, stats,
+                                           o, cache, new_lens, acc, pos, seen, workspace,
+                                           workspace_bytes, stream)
+
+
+def bpt_layer_backward_window_workspace_size(B, N, d, h, d_ff, dtype, window,
+                                             sinks) -> Tuple[int, int]:
+    """Returns (status, bytes)."""
+    out = ctypes.c_size_t(0)
+    st = load().bpt_layer_backward_window_workspace_size(B, N, d, h, d_ff, dtype, window, sinks,
+                                                         ctypes.byref(out))
+    return st, out.value
+
+
+def bpt_layer_backward_window(x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, stats, o, dZ, B,
+                              N, d, h, d_ff, dtype, window, sinks, lens, dx, d_ln1, dW_Q, dW_K,
+                              dW_V, dW_O, d_ln2, dW_1, db_1, dW_2, db_2, workspace,
+                              workspace_bytes, stream) -> int:
+    """Pointer-level call (lens may be None); returns the status."""
+    return load().bpt_layer_backward_window(x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2,
+                                            stats, o, dZ, B, N, d, h, d_ff, dtype, window, sinks,
+                                            lens, dx, d_ln1, dW_Q, dW_K, dW_V, dW_O, d_ln2, dW_1,
+                                            db_1, dW_2, db_2, workspace, workspace_bytes, stream)
+
+
+def bpt_layer_decode_workspace_size(cache: Cache, d, d_ff, with_acc) -> Tuple[int, int]:
+    """Returns (status, bytes)."""
+    out = ctypes.c_size_t(0)
+    st = load().bpt_layer_decode_workspace_size(ctypes.byref(cache), d, d_ff, int(bool(with_acc)),
+                                                ctypes.byref(out))
+    return st, out.value
+
+
+def bpt_layer_decode_prepare(W_Q, W_K, W_V, W_O, W_1, W_2, cache, d, d_ff, with_acc, workspace,
+                             workspace_bytes, stream) -> int:
+    """Pointer-level call; returns the status."""
+    return load().bpt_layer_decode_prepare(W_Q, W_K, W_V, W_O, W_1, W_2, cache, d, d_ff,
+                                           int(bool(with_acc)), workspace, workspace_bytes, stream)
+
+
+def bpt_layer_decode(x, ln1, ln2, b_1, b_2, cache, d, d_ff, window, sinks, acc, pos, seen, new_lens,
+                     out, workspace, workspace_bytes, stream) -> int:
+    """Pointer-level call (acc, pos, seen may be None); returns the status."""
+    return load().bpt_layer_decode(x, ln1, ln2, b_1, b_2, cache, d, d_ff, window, sinks, acc, pos,
+                                   seen, new_lens, out, workspace, workspace_bytes, stream)

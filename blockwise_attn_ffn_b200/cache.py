@@ -77,7 +77,8 @@ def rows_check(t: torch.Tensor, what: str, shape: tuple, dtype, index: int) -> i
     return t.data_ptr()
 
 
-def _cache(k_cache, v_cache, page_table, lens) -> "_lib.Cache":
+def cache_struct(k_cache, v_cache, page_table, lens) -> "_lib.Cache":
+    """The C struct of a cache, its tensors checked."""
     if k_cache.dim() != 4 or not k_cache.is_cuda or not k_cache.is_contiguous():
         raise ValueError("k_cache must be a contiguous CUDA tensor [pages, kv_heads, page_size, d_k]")
     index = k_cache.get_device()
@@ -93,7 +94,7 @@ def _cache(k_cache, v_cache, page_table, lens) -> "_lib.Cache":
                       B, pages, hkv, ps, dk, per, code, 0)
 
 
-def _sizes(k_cache, page_table) -> "_lib.Cache":
+def cache_sizes(k_cache, page_table) -> "_lib.Cache":
     """The cache's sizes alone, for the workspace calls."""
     if k_cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_cache must be [pages, kv_heads, page_size, d_k], page_table "
@@ -106,7 +107,7 @@ def _sizes(k_cache, page_table) -> "_lib.Cache":
 
 def cache_workspace(k_cache: torch.Tensor, page_table: torch.Tensor) -> torch.Tensor:
     """A workspace for ``cache_append`` and ``cache_evict`` on this cache."""
-    st, nbytes = _lib.bpt_cache_workspace_size(_sizes(k_cache, page_table))
+    st, nbytes = _lib.bpt_cache_workspace_size(cache_sizes(k_cache, page_table))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_cache_workspace_size")
     return new_workspace(nbytes, k_cache.device)
@@ -115,7 +116,7 @@ def cache_workspace(k_cache: torch.Tensor, page_table: torch.Tensor) -> torch.Te
 def attn_decode_workspace(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Tensor,
                           with_acc: bool = False) -> torch.Tensor:
     """A workspace for ``attn_decode`` with these queries and this cache."""
-    st, nbytes = _lib.bpt_attn_decode_workspace_size(_sizes(k_cache, page_table), q.shape[1],
+    st, nbytes = _lib.bpt_attn_decode_workspace_size(cache_sizes(k_cache, page_table), q.shape[1],
                                                      with_acc)
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_decode_workspace_size")
@@ -131,7 +132,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     """Writes the new tokens k, v [B, T, kv_heads, d_k] (any strides that are
     multiples of 8 elements, last dimension contiguous) behind each sequence;
     returns new_lens [B] (allocated if not given; not the lens tensor)."""
-    c = _cache(k_cache, v_cache, page_table, lens)
+    c = cache_struct(k_cache, v_cache, page_table, lens)
     index, dt, B = k_cache.get_device(), k_cache.dtype, lens.shape[0]
     if k.dim() != 4:
         raise ValueError("k must be [B, T, kv_heads, d_k]")
@@ -163,7 +164,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     """Attention of one new token per sequence, q [B, heads, d_k], over the
     cache; returns out [B, heads, d_k].  With acc, the weight every slot
     received is added: acc_out = acc + weights (acc_out None: in place)."""
-    c = _cache(k_cache, v_cache, page_table, lens)
+    c = cache_struct(k_cache, v_cache, page_table, lens)
     index, dt, B = k_cache.get_device(), k_cache.dtype, lens.shape[0]
     if q.dim() != 3:
         raise ValueError("q must be [B, heads, d_k]")
@@ -201,7 +202,7 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.
     first ``sinks`` and the last ``recent`` positions and then the largest
     accumulated weights, and packs the rest; returns new_lens.  acc_out,
     pos_out, new_lens None: updated in place."""
-    c = _cache(k_cache, v_cache, page_table, lens)
+    c = cache_struct(k_cache, v_cache, page_table, lens)
     index, B = k_cache.get_device(), lens.shape[0]
     slots = (B, k_cache.shape[1], page_table.shape[1] * k_cache.shape[2])
     ap = check(acc, "acc", slots, torch.float32, index)

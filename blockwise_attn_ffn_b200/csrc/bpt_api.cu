@@ -31,6 +31,7 @@
 #include <vector>
 
 #include "bpt.h"
+#include "ops_internal.h"
 #include "attn_bwd_tc.cuh"
 #include "attn_pair_tc.cuh"
 #include "attn_b64_tc.cuh"
@@ -630,12 +631,98 @@ struct ShardSpec {
   const void* kv_all; // phase 2: [G, B, n_loc, 2d]
 };
 
+// What the attention of a bf16 forward does instead of the dense kernel: a
+// sliding window (bpt_layer_forward_window) or one new token per sequence over
+// a cache (bpt_layer_decode, waves schedule, the plan's N tokens are the
+// sequences).
+struct AttnForm {
+  int64_t window, sinks;
+  const int32_t* lens;      // window: nullable
+  const bpt_cache* cache;   // window: nullable, the prompt's K and V are appended
+  int32_t* new_lens;
+  bool decode;
+  float* acc;               // decode: nullable, updated in place
+  int32_t* pos;             // decode: nullable
+  const int32_t* seen;
+  uint8_t* ws;              // decode: workspace of bpt_attn_decode
+  size_t ws_bytes;
+};
+
+// The fused layer body over every query block (the tensor maps of its A and B
+// operands: o, W_O, LN2(y), W_1, H, W_2, and H / W_2 in 64-deep boxes).
+bpt_status launch_tail(const Plan& P, int pairs_max, const CUtensorMap& mO, const CUtensorMap& mWo,
+                       const CUtensorMap& mV, const CUtensorMap& mW1, const CUtensorMap& mH,
+                       const CUtensorMap& mW2, const CUtensorMap& mH1, const CUtensorMap& mW2e,
+                       const void* x, const void* ln2, const void* b_1, const void* b_2,
+                       float* out, uint8_t* ws, cudaStream_t s) {
+  using bf = __nv_bfloat16;
+  using hf = __half;
+  const int64_t d = P.d, d_ff = P.d_ff;
+  bpt::TailParams tp{};
+  tp.blocks = int(P.items);
+  tp.items = int((P.items + 1) / 2);
+  tp.nb = int(P.nb);
+  tp.N = int(P.N);
+  tp.d = int(d);
+  tp.d_ff = int(d_ff);
+  tp.out = out;
+  tp.x = static_cast<const bf*>(x);
+  tp.ln2 = static_cast<const bf*>(ln2);
+  tp.b1 = static_cast<const bf*>(b_1);
+  tp.b2 = static_cast<const bf*>(b_2);
+  tp.v_scr = reinterpret_cast<hf*>(ws + P.off_tv);
+  tp.h_scr = reinterpret_cast<hf*>(ws + P.off_th);
+  tp.err = reinterpret_cast<uint32_t*>(ws);
+  tp.fault = P.opt.fault == 3 ? 3 : 0;
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(P.tail_pairs, pairs_max));
+  // Share the items left over after the whole rounds between two pairs
+  // each when at most half of the pairs would otherwise work in the last
+  // round and every half is a whole number of tiles (y tiles and H chunks
+  // of 256 columns, Z tiles of 512).
+  tp.split = (BPT_TAIL_SHARE_ITEMS && bpt::tail_shares(tp.items, int(pairs), int(d), int(d_ff)))
+                 ? 1 : 0;
+  tp.flags = reinterpret_cast<uint32_t*>(ws + kTailFlagOffset);
+  if (tp.split) {
+    // Under stream capture (a CUDA graph being recorded) the body runs
+    // unshared with a plain launch, which graphs always accept.
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return BPT_ERR_CUDA;
+    if (cap != cudaStreamCaptureStatusNone) tp.split = 0;
+  }
+  LaunchScope ls(BPT_KIND_TAIL, s);
+  if (tp.split) {
+    // A pair waits for its partner's hand-overs, so all pairs must be
+    // resident at once: a cooperative launch guarantees it (or fails, and
+    // the layer body runs without sharing).
+    if (cudaMemsetAsync(tp.flags, 0, kTailFlagBytes, s) != cudaSuccess) return BPT_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(2 * pairs));
+    cfg.blockDim = dim3(bpt::kTailThreads);
+    cfg.dynamicSmemBytes = bpt::kPairSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, bpt::tail_pair_kernel, mO, mWo, mV, mW1, mH, mW2, mH1, mW2e,
+                           tp) == cudaSuccess)
+      return BPT_OK;
+    (void)cudaGetLastError();
+    tp.split = 0;
+  }
+  bpt::tail_pair_kernel<<<unsigned(2 * pairs), bpt::kTailThreads, bpt::kPairSmem, s>>>(
+      mO, mWo, mV, mW1, mH, mW2, mH1, mW2e, tp);
+  if (cudaGetLastError() != cudaSuccess) return BPT_ERR_CUDA;
+  return BPT_OK;
+}
+
 bpt_status forward_bf16(const Plan& P, const void* x, const void* ln1, const void* W_Q,
                         const void* W_K, const void* W_V, const void* W_O, const void* ln2,
                         const void* W_1, const void* b_1, const void* W_2, const void* b_2,
                         float* out, float* stats, uint8_t* ws, cudaStream_t s, int sms,
                         const AttnGate* gate, const ShardSpec* shard = nullptr,
-                        __half* o_keep = nullptr) {
+                        __half* o_keep = nullptr, const AttnForm* form = nullptr) {
   using bf = __nv_bfloat16;
   using hf = __half;
   const int64_t M = P.B * P.N, d = P.d, d_ff = P.d_ff;
@@ -687,7 +774,7 @@ bpt_status forward_bf16(const Plan& P, const void* x, const void* ln1, const voi
 
   RowMap ident{0, 1, 1, 1, 1};
   if (shard == nullptr || shard->phase == 1) {
-  {
+  if (form == nullptr || !form->decode) {  // (a decode step's weights are prepared)
     bpt::CvtSegments cs{};
     const void* src[6] = {W_Q, W_K, W_V, W_O, W_1, W_2};
     hf* dst[6] = {wq, wk, wv, wo, w1, w2};
@@ -730,6 +817,31 @@ bpt_status forward_bf16(const Plan& P, const void* x, const void* ln1, const voi
   }
   }  // projection
   if (shard != nullptr && shard->phase == 1) return BPT_OK;
+  const int64_t heads_stride[6] = {P.N * 3 * d, 3 * d, P.dk, P.N * 3 * d, 3 * d, P.dk};
+  if (form != nullptr && !form->decode) {
+    // windowed attention of whole sequences: o beside the projection (o_keep)
+    {
+      bpt_window w{P.B, P.N, P.N, P.h, P.h, P.dk, form->window, form->sinks, BPT_F16, 0};
+      const bpt_rows rq{qkv, P.N * 3 * d, 3 * d, P.dk}, rk{qkv + d, P.N * 3 * d, 3 * d, P.dk},
+          rv{qkv + 2 * d, P.N * 3 * d, 3 * d, P.dk}, ro{o_keep, P.N * d, d, P.dk};
+      LaunchScope ls(BPT_KIND_ATTN, s);
+      const bpt_status st =
+          bpt_host::window_forward(&w, &rq, &rk, &rv, form->lens, &ro, stats, ws, kHeaderBytes,
+                                   reinterpret_cast<bpt_stream_t>(s), err);
+      if (st != BPT_OK) return st;
+    }
+    if (form->cache != nullptr) {
+      const bpt_status st = bpt_host::cache_append(
+          form->cache, qkv + d, qkv + 2 * d, P.N, heads_stride, form->lens, form->new_lens,
+          form->acc, form->pos, form->seen, ws, kHeaderBytes, reinterpret_cast<bpt_stream_t>(s),
+          err);
+      if (st != BPT_OK) return st;
+    }
+    int sms_ = 0, pairs_ = 0;
+    if (device_info(&sms_, &pairs_) != BPT_OK) return BPT_ERR_CUDA;
+    return launch_tail(P, pairs_, mO, mWo, mV, mW1, mH, mW2, mH1, mW2e, x, ln2, b_1, b_2, out, ws,
+                       s);
+  }
   if (P.fused) {
     // attention over every query block, o over each block's Q rows
     const Wave all{0, P.items, P.B};
@@ -751,69 +863,29 @@ bpt_status forward_bf16(const Plan& P, const void* x, const void* ln1, const voi
     }
     int dummy = 0, pairs_max = 0;
     if (device_info(&dummy, &pairs_max) != BPT_OK) return BPT_ERR_CUDA;
-    bpt::TailParams tp{};
-    tp.blocks = int(P.items);
-    tp.items = int((P.items + 1) / 2);
-    tp.nb = int(P.nb);
-    tp.N = int(P.N);
-    tp.d = int(d);
-    tp.d_ff = int(d_ff);
-    tp.out = out;
-    tp.x = static_cast<const bf*>(x);
-    tp.ln2 = static_cast<const bf*>(ln2);
-    tp.b1 = static_cast<const bf*>(b_1);
-    tp.b2 = static_cast<const bf*>(b_2);
-    tp.v_scr = reinterpret_cast<hf*>(ws + P.off_tv);
-    tp.h_scr = reinterpret_cast<hf*>(ws + P.off_th);
-    tp.err = err;
-    tp.fault = fault == 3 ? 3 : 0;
-    const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(P.tail_pairs, pairs_max));
-    // Share the items left over after the whole rounds between two pairs
-    // each when at most half of the pairs would otherwise work in the last
-    // round and every half is a whole number of tiles (y tiles and H chunks
-    // of 256 columns, Z tiles of 512).
-    tp.split = (BPT_TAIL_SHARE_ITEMS && bpt::tail_shares(tp.items, int(pairs), int(d), int(d_ff)))
-                   ? 1 : 0;
-    tp.flags = reinterpret_cast<uint32_t*>(ws + kTailFlagOffset);
-    if (tp.split) {
-      // Under stream capture (a CUDA graph being recorded) the body runs
-      // unshared with a plain launch, which graphs always accept.
-      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-      if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return BPT_ERR_CUDA;
-      if (cap != cudaStreamCaptureStatusNone) tp.split = 0;
-    }
-    LaunchScope ls(BPT_KIND_TAIL, s);
-    if (tp.split) {
-      // A pair waits for its partner's hand-overs, so all pairs must be
-      // resident at once: a cooperative launch guarantees it (or fails, and
-      // the layer body runs without sharing).
-      if (cudaMemsetAsync(tp.flags, 0, kTailFlagBytes, s) != cudaSuccess) return BPT_ERR_CUDA;
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(unsigned(2 * pairs));
-      cfg.blockDim = dim3(bpt::kTailThreads);
-      cfg.dynamicSmemBytes = bpt::kPairSmem;
-      cfg.stream = s;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeCooperative;
-      attr[0].val.cooperative = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaLaunchKernelEx(&cfg, bpt::tail_pair_kernel, mO, mWo, mV, mW1, mH, mW2, mH1, mW2e,
-                             tp) == cudaSuccess)
-        return BPT_OK;
-      (void)cudaGetLastError();
-      tp.split = 0;
-    }
-    bpt::tail_pair_kernel<<<unsigned(2 * pairs), bpt::kTailThreads, bpt::kPairSmem, s>>>(
-        mO, mWo, mV, mW1, mH, mW2, mH1, mW2e, tp);
-    if (cudaGetLastError() != cudaSuccess) return BPT_ERR_CUDA;
-    return BPT_OK;
+    return launch_tail(P, pairs_max, mO, mWo, mV, mW1, mH, mW2, mH1, mW2e, x, ln2, b_1, b_2, out,
+                       ws, s);
   }
   for (int64_t w = 0; w < P.n_waves; ++w) {
     const Wave wv_ = P.wave(w);
     const int64_t rows = wv_.count * P.blk;
     RowMap map{int(wv_.item0), int(P.nb), int(P.N), int(P.blk), 0};
-    {
+    if (form != nullptr) {
+      // a decode step (one wave: token rows are block rows): the new K and V
+      // into the cache, then each token's attention over its sequence
+      bpt_cache c = *form->cache;
+      const bpt_stream_t st_ = reinterpret_cast<bpt_stream_t>(s);
+      const int64_t kv_stride[6] = {3 * d, 3 * d, P.dk, 3 * d, 3 * d, P.dk};
+      LaunchScope ls(BPT_KIND_ATTN, s);
+      bpt_status st = bpt_host::cache_append(&c, qkv + d, qkv + 2 * d, 1, kv_stride, nullptr,
+                                             form->new_lens, form->acc, form->pos, form->seen, ws,
+                                             kHeaderBytes, st_, err);
+      if (st != BPT_OK) return st;
+      c.lens = form->new_lens;
+      st = bpt_host::attn_decode(&c, qkv, P.h, 3 * d, P.dk, form->window, form->sinks, form->acc,
+                                 form->acc, so, d, P.dk, form->ws, form->ws_bytes, st_, err);
+      if (st != BPT_OK) return st;
+    } else {
       LaunchScope ls(BPT_KIND_ATTN, s);
       if (launch_attn(P, wv_, mQKV, so, stats, err, (fault == 2 && w == 0) ? 2 : 0, s, gate,
                       false, nullptr, &mQKVh) !=
@@ -1184,7 +1256,8 @@ bpt_status backward_bf16(const Plan& P, const BwdLayout& L, const void* x, const
                          const float* stats, const float* dZ, float* dx, float* d_ln1,
                          float* dW_Q, float* dW_K, float* dW_V, float* dW_O, float* d_ln2,
                          float* dW_1, float* db_1, float* dW_2, float* db_2, uint8_t* ws,
-                         cudaStream_t s, int sms, const __half* o_keep) {
+                         cudaStream_t s, int sms, const __half* o_keep,
+                         const AttnForm* form = nullptr) {
   using bf = __nv_bfloat16;
   using hf = __half;
   const int64_t M = P.B * P.N, d = P.d, d_ff = P.d_ff, h = P.h;
@@ -1352,6 +1425,16 @@ bpt_status backward_bf16(const Plan& P, const BwdLayout& L, const void* x, const
     if (!gemm(mDyA, mWok, rows, d, d, bpt::kEpiStoreF16, bpt::kLayAkBk, ident,
               [&](bpt::GemmParams& g) { g.out_h = do16; g.ld_out = d; }))
       return BPT_ERR_CUDA;
+    if (form != nullptr) {
+      // windowed attention: dO of every row is gathered (where dQ would go),
+      // its backward runs once, after the waves
+      bpt::rows_copy_f16_kernel<<<unsigned(std::min<int64_t>((rows * d / 8 + 255) / 256,
+                                                             int64_t(sms) * 16)),
+                                  256, 0, s>>>(do16, d, reinterpret_cast<hf*>(dq), d, rows,
+                                               int(d), map, 1);
+      if (cudaGetLastError() != cudaSuccess) return BPT_ERR_CUDA;
+      continue;
+    }
     // attention backward of this wave's query rows
     bpt::attn_row_terms_kernel<<<unsigned((rows * 32 + 255) / 256), 256, 0, s>>>(
         do16, so, reinterpret_cast<const float2*>(stats), qs, rows, int(d), int(h), map);
@@ -1379,9 +1462,22 @@ bpt_status backward_bf16(const Plan& P, const BwdLayout& L, const void* x, const
     if (cudaGetLastError() != cudaSuccess) return BPT_ERR_CUDA;
   }
   // QKV projection and LN1 backward over all rows
-  bpt::pack3_f32_to_f16_kernel<<<unsigned(std::min<int64_t>((M * 3 * d / 8 + 255) / 256,
-                                                           int64_t(sms) * 16)),
-                                 256, 0, s>>>(dq, dk, dv, dqkv16, M, int(d));
+  if (form != nullptr) {
+    bpt_window w{P.B, P.N, P.N, P.h, P.h, P.dk, form->window, form->sinks, BPT_F16, 0};
+    const int64_t nb3 = P.N * 3 * d, n3 = 3 * d, nb1 = P.N * d;
+    const bpt_rows rq{qkv, nb3, n3, P.dk}, rk{qkv + d, nb3, n3, P.dk},
+        rv{qkv + 2 * d, nb3, n3, P.dk}, ro{const_cast<hf*>(o_keep), nb1, d, P.dk},
+        rdo{dq, nb1, d, P.dk}, gq{dqkv16, nb3, n3, P.dk}, gk{dqkv16 + d, nb3, n3, P.dk},
+        gv{dqkv16 + 2 * d, nb3, n3, P.dk};
+    const bpt_status st = bpt_host::window_backward(
+        &w, &rq, &rk, &rv, &ro, stats, &rdo, form->lens, &gq, &gk, &gv, form->ws, form->ws_bytes,
+        reinterpret_cast<bpt_stream_t>(s), err);
+    if (st != BPT_OK) return st;
+  } else {
+    bpt::pack3_f32_to_f16_kernel<<<unsigned(std::min<int64_t>((M * 3 * d / 8 + 255) / 256,
+                                                             int64_t(sms) * 16)),
+                                   256, 0, s>>>(dq, dk, dv, dqkv16, M, int(d));
+  }
   float* dWqkv[3] = {dW_Q, dW_K, dW_V};
   for (int i = 0; i < 3; ++i) {
     if (!gemm(mUt, mDqB[i], d, d, M, bpt::kEpiAccumF32, bpt::kLayAnBn, ident,
@@ -1430,7 +1526,7 @@ bpt_status layer_forward_impl(const void* x, const void* ln1, const void* W_Q, c
                               bpt_dtype dtype, float* out, float* stats, void* workspace,
                               size_t workspace_bytes, const bpt_options* opts,
                               bpt_stream_t stream, const AttnGate* gate = nullptr,
-                              void* o_keep = nullptr) {
+                              void* o_keep = nullptr, const AttnForm* form = nullptr) {
   bpt_status st = check_shape(B, N, d, h, d_ff, causal, dtype);
   if (st != BPT_OK) return st;
   Opts opt;
@@ -1445,12 +1541,47 @@ bpt_status layer_forward_impl(const void* x, const void* ln1, const void* W_Q, c
   for (const void* p : ptrs)
     if (p == nullptr || misaligned(p)) return BPT_ERR_INVALID_ARG;
   const Plan P = make_plan(B, N, d, h, d_ff, causal, dtype, opt);
-  if (workspace_bytes < P.total) return BPT_ERR_WORKSPACE;
+  // windowed: the attention output, unless the caller keeps it, follows the plan's regions
+  const size_t ws_need =
+      P.total + (form != nullptr && o_keep == nullptr ? size_t(B * N * d) * 2 : 0);
+  if (workspace_bytes < ws_need) return BPT_ERR_WORKSPACE;
   // out and the workspace are written while the inputs are still read: they
   // must overlap no input and not each other; stats likewise.
-  const std::vector<Span> ins =
+  std::vector<Span> ins =
       forward_inputs(x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, B, N, d, d_ff, P.esize);
-  const Span so(out, size_t(B * N * d) * 4), sw(workspace, P.total);
+  if (form != nullptr && form->lens != nullptr) ins.push_back(Span(form->lens, size_t(B) * 4));
+  if (form != nullptr) {
+    bpt_window w{B, N, N, h, h, P.dk, form->window, form->sinks, BPT_F16, 0};
+    size_t bytes = 0;
+    st = bpt_attn_window_workspace_size(&w, &bytes);
+    if (st != BPT_OK) return st;
+  }
+  if (form != nullptr && form->cache != nullptr) {
+    const bpt_cache& c = *form->cache;
+    const __half* kv = reinterpret_cast<const __half*>(static_cast<const uint8_t*>(workspace) +
+                                                       P.off_qkv) + d;
+    const int64_t st6[6] = {N * 3 * d, 3 * d, P.dk, N * 3 * d, 3 * d, P.dk};
+    st = bpt_host::cache_append(&c, kv, kv + d, N, st6, form->lens, form->new_lens, form->acc,
+                                form->pos, form->seen, workspace, kHeaderBytes, stream, nullptr,
+                                true);
+    if (st != BPT_OK) return st;
+    const size_t rows = size_t(c.pages) * size_t(c.kv_heads * c.page_size) * size_t(c.d_k) * 2;
+    const size_t slots = size_t(B * c.kv_heads) * size_t(c.max_pages * c.page_size) * 4;
+    // the append writes these while the layer's inputs are still to be read
+    for (const Span& sp : {Span(c.k, rows), Span(c.v, rows), Span(form->new_lens, size_t(B) * 4),
+                           Span(form->acc, form->acc ? slots : 0),
+                           Span(form->pos, form->pos ? slots : 0)})
+      for (const Span& in : ins)
+        if (sp.overlaps(in)) return BPT_ERR_INVALID_ARG;
+    for (const Span& sp : {Span(c.k, rows), Span(c.v, rows), Span(c.lens, size_t(B) * 4),
+                           Span(c.page_table, size_t(B * c.max_pages) * 4),
+                           Span(form->new_lens, size_t(B) * 4),
+                           Span(form->acc, form->acc ? slots : 0),
+                           Span(form->pos, form->pos ? slots : 0),
+                           Span(form->seen, form->seen ? size_t(B) * 4 : 0)})
+      ins.push_back(sp);
+  }
+  const Span so(out, size_t(B * N * d) * 4), sw(workspace, ws_need);
   if (so.overlaps(sw)) return BPT_ERR_INVALID_ARG;
   for (const Span& in : ins)
     if (so.overlaps(in) || sw.overlaps(in)) return BPT_ERR_INVALID_ARG;
@@ -1479,8 +1610,9 @@ bpt_status layer_forward_impl(const void* x, const void* ln1, const void* W_Q, c
   if (dtype == BPT_BF16) {
     st = get_encoder();
     if (st != BPT_OK) return st;
+    if (form != nullptr && o_keep == nullptr) o_keep = ws + P.total;
     return forward_bf16(P, x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, out, stats, ws, s,
-                        sms, gate, nullptr, static_cast<__half*>(o_keep));
+                        sms, gate, nullptr, static_cast<__half*>(o_keep), form);
   }
   return forward_f32(P, static_cast<const float*>(x), static_cast<const float*>(ln1),
                      static_cast<const float*>(W_Q), static_cast<const float*>(W_K),
@@ -1540,7 +1672,7 @@ bpt_status backward_impl(const void* x, const void* ln1, const void* W_Q, const 
                          float* dW_Q, float* dW_K, float* dW_V, float* dW_O, float* d_ln2,
                          float* dW_1, float* db_1, float* dW_2, float* db_2, void* workspace,
                          size_t workspace_bytes, const bpt_options* opts, bpt_stream_t stream,
-                         const void* o_keep = nullptr) {
+                         const void* o_keep = nullptr, const AttnForm* form = nullptr) {
   (void)b_2;  // the output's bias does not enter any gradient but its own
   bpt_status st = check_shape(B, N, d, h, d_ff, causal, dtype);
   if (st != BPT_OK) return st;
@@ -1559,8 +1691,17 @@ bpt_status backward_impl(const void* x, const void* ln1, const void* W_Q, const 
                               size_t(2 * d) * 4, size_t(d * d_ff) * 4, size_t(d_ff) * 4,
                               size_t(d_ff * d) * 4, size_t(d) * 4};
   const Plan P = make_plan(B, N, d, h, d_ff, causal, dtype, opt, false);
-  const size_t ws_need =
-      dtype == BPT_BF16 ? make_bwd_layout(P).total : make_bwd_layout_f32(P).total;
+  size_t ws_need = dtype == BPT_BF16 ? make_bwd_layout(P).total : make_bwd_layout_f32(P).total;
+  AttnForm wform{};
+  if (form != nullptr) {
+    wform = *form;
+    bpt_window w{B, N, N, h, h, P.dk, form->window, form->sinks, BPT_F16, 0};
+    st = bpt_attn_window_backward_workspace_size(&w, &wform.ws_bytes);
+    if (st != BPT_OK) return st;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return BPT_ERR_INVALID_ARG;
+    wform.ws = static_cast<uint8_t*>(workspace) + ws_need;
+    ws_need += wform.ws_bytes;
+  }
   if (workspace_bytes < ws_need) return BPT_ERR_WORKSPACE;
   // Outputs must be aligned and must not overlap each other, the workspace,
   // or any input (every input is read after some output is first written).
@@ -1572,6 +1713,7 @@ bpt_status backward_impl(const void* x, const void* ln1, const void* W_Q, const 
     if (misaligned(o_keep)) return BPT_ERR_INVALID_ARG;
     reads.push_back(Span(o_keep, size_t(B * N * d) * 2));
   }
+  if (form != nullptr && form->lens != nullptr) reads.push_back(Span(form->lens, size_t(B) * 4));
   const Span sw(workspace, ws_need);
   for (const Span& r : reads)
     if (sw.overlaps(r)) return BPT_ERR_INVALID_ARG;
@@ -1601,7 +1743,7 @@ bpt_status backward_impl(const void* x, const void* ln1, const void* W_Q, const 
   const BwdLayout L = make_bwd_layout(P);
   return backward_bf16(P, L, x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, stats, dZ, dx, d_ln1,
                        dW_Q, dW_K, dW_V, dW_O, d_ln2, dW_1, db_1, dW_2, db_2, ws, s, sms,
-                       static_cast<const __half*>(o_keep));
+                       static_cast<const __half*>(o_keep), form != nullptr ? &wform : nullptr);
 }
 
 // Shared body of the sequence-shard entry points (phase 1: projection into
@@ -1909,6 +2051,245 @@ bpt_status bpt_layer_shard_forward(const void* x, const void* ln1, const void* W
   return shard_impl(2, x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, B, N, G, rank, d, h,
                     d_ff, causal, dtype, const_cast<void*>(kv_all), out, workspace,
                     workspace_bytes, stream);
+}
+
+// ----------------------------------------------- window and cache forms --
+bpt_status bpt_layer_forward_window_workspace_size(int64_t B, int64_t N, int64_t d, int64_t h,
+                                                   int64_t d_ff, bpt_dtype dtype, size_t* bytes) {
+  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
+  if (dtype != BPT_BF16) return dtype == BPT_F32 ? BPT_ERR_UNSUPPORTED : BPT_ERR_INVALID_ARG;
+  Plan P;
+  const bpt_status st = plan_for(B, N, d, h, d_ff, 1, dtype, nullptr, true, &P);
+  if (st != BPT_OK) return st;
+  *bytes = P.total + size_t(B * N * d) * 2;
+  return BPT_OK;
+}
+
+bpt_status bpt_layer_forward_window(const void* x, const void* ln1, const void* W_Q,
+                                    const void* W_K, const void* W_V, const void* W_O,
+                                    const void* ln2, const void* W_1, const void* b_1,
+                                    const void* W_2, const void* b_2, int64_t B, int64_t N,
+                                    int64_t d, int64_t h, int64_t d_ff, bpt_dtype dtype,
+                                    int64_t window, int64_t sinks, const int32_t* lens, float* out,
+                                    float* stats, void* o, const bpt_cache* cache,
+                                    int32_t* new_lens, float* acc, int32_t* pos,
+                                    const int32_t* seen, void* workspace, size_t workspace_bytes,
+                                    bpt_stream_t stream) {
+  if (window <= 0 || sinks < 0) return BPT_ERR_INVALID_ARG;
+  if (dtype != BPT_BF16) return dtype == BPT_F32 ? BPT_ERR_UNSUPPORTED : BPT_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(lens) & 3u))
+    return BPT_ERR_INVALID_ARG;
+  if (cache != nullptr) {
+    // everything the append would refuse is refused before anything runs
+    if (cache->dtype != BPT_F16 || cache->batch != B || cache->kv_heads != h ||
+        cache->d_k * h != d || new_lens == nullptr)
+      return BPT_ERR_INVALID_ARG;
+  } else if (new_lens != nullptr || acc != nullptr || pos != nullptr || seen != nullptr) {
+    return BPT_ERR_INVALID_ARG;
+  }
+  AttnForm form{};
+  form.window = window;
+  form.sinks = sinks;
+  form.lens = lens;
+  form.cache = cache;
+  form.new_lens = new_lens;
+  form.acc = acc;
+  form.pos = pos;
+  form.seen = seen;
+  return layer_forward_impl(x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, B, N, d, h, d_ff,
+                            1, dtype, out, stats, workspace, workspace_bytes, nullptr, stream,
+                            nullptr, o, &form);
+}
+
+bpt_status bpt_layer_backward_window_workspace_size(int64_t B, int64_t N, int64_t d, int64_t h,
+                                                    int64_t d_ff, bpt_dtype dtype, int64_t window,
+                                                    int64_t sinks, size_t* bytes) {
+  if (bytes == nullptr || window <= 0 || sinks < 0) return BPT_ERR_INVALID_ARG;
+  if (dtype != BPT_BF16) return dtype == BPT_F32 ? BPT_ERR_UNSUPPORTED : BPT_ERR_INVALID_ARG;
+  Plan P;
+  bpt_status st = plan_for(B, N, d, h, d_ff, 1, dtype, nullptr, false, &P);
+  if (st != BPT_OK) return st;
+  bpt_window w{B, N, N, h, h, P.dk, window, sinks, BPT_F16, 0};
+  size_t attn = 0;
+  st = bpt_attn_window_backward_workspace_size(&w, &attn);
+  if (st != BPT_OK) return st;
+  *bytes = make_bwd_layout(P).total + attn;
+  return BPT_OK;
+}
+
+bpt_status bpt_layer_backward_window(const void* x, const void* ln1, const void* W_Q,
+                                     const void* W_K, const void* W_V, const void* W_O,
+                                     const void* ln2, const void* W_1, const void* b_1,
+                                     const void* W_2, const void* b_2, const float* stats,
+                                     const void* o, const float* dZ, int64_t B, int64_t N,
+                                     int64_t d, int64_t h, int64_t d_ff, bpt_dtype dtype,
+                                     int64_t window, int64_t sinks, const int32_t* lens, float* dx,
+                                     float* d_ln1, float* dW_Q, float* dW_K, float* dW_V,
+                                     float* dW_O, float* d_ln2, float* dW_1, float* db_1,
+                                     float* dW_2, float* db_2, void* workspace,
+                                     size_t workspace_bytes, bpt_stream_t stream) {
+  if (window <= 0 || sinks < 0 || o == nullptr) return BPT_ERR_INVALID_ARG;
+  if (dtype != BPT_BF16) return dtype == BPT_F32 ? BPT_ERR_UNSUPPORTED : BPT_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(lens) & 3u) return BPT_ERR_INVALID_ARG;
+  AttnForm form{};
+  form.window = window;
+  form.sinks = sinks;
+  form.lens = lens;
+  return backward_impl(x, ln1, W_Q, W_K, W_V, W_O, ln2, W_1, b_1, W_2, b_2, stats, dZ, B, N, d, h,
+                       d_ff, 1, dtype, dx, d_ln1, dW_Q, dW_K, dW_V, dW_O, d_ln2, dW_1, db_1, dW_2,
+                       db_2, workspace, workspace_bytes, nullptr, stream, o, &form);
+}
+
+namespace {
+
+// A decode step's plan: the batch's new tokens as one sequence of `batch`
+// rows on the waves schedule (one wave; the fused body would leave all but a
+// pair of SMs idle), then the workspace of its attention.
+struct DecodePlan {
+  Plan P;
+  size_t off_attn, attn_bytes, total;
+};
+bpt_status decode_plan(const bpt_cache* c, int64_t d, int64_t d_ff, int with_acc, DecodePlan* r) {
+  if (c == nullptr || c->dtype != BPT_F16 || c->batch < 0 || c->kv_heads <= 0 ||
+      c->d_k * c->kv_heads != d)
+    return BPT_ERR_INVALID_ARG;
+  if (c->batch > BPT_WAVE_BLOCKS * 128) return BPT_ERR_UNSUPPORTED;
+  bpt_status st = check_shape(1, c->batch, d, c->kv_heads, d_ff, 1, BPT_BF16);
+  if (st != BPT_OK) return st;
+  Opts opt;
+  opt.fused = 0;
+  r->P = make_plan(1, c->batch, d, c->kv_heads, d_ff, 1, BPT_BF16, opt);
+  st = bpt_attn_decode_workspace_size(c, c->kv_heads, with_acc, &r->attn_bytes);
+  if (st != BPT_OK) return st;
+  r->off_attn = align_up(r->P.total, 1024);
+  r->total = r->off_attn + r->attn_bytes;
+  return BPT_OK;
+}
+
+}  // namespace
+
+bpt_status bpt_layer_decode_workspace_size(const bpt_cache* cache, int64_t d, int64_t d_ff,
+                                           int with_acc, size_t* bytes) {
+  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
+  DecodePlan dp;
+  const bpt_status st = decode_plan(cache, d, d_ff, with_acc, &dp);
+  if (st != BPT_OK) return st;
+  *bytes = dp.total;
+  return BPT_OK;
+}
+
+bpt_status bpt_layer_decode_prepare(const void* W_Q, const void* W_K, const void* W_V,
+                                    const void* W_O, const void* W_1, const void* W_2,
+                                    const bpt_cache* cache, int64_t d, int64_t d_ff, int with_acc,
+                                    void* workspace, size_t workspace_bytes, bpt_stream_t stream) {
+  DecodePlan dp;
+  bpt_status st = decode_plan(cache, d, d_ff, with_acc, &dp);
+  if (st != BPT_OK) return st;
+  const void* src[6] = {W_Q, W_K, W_V, W_O, W_1, W_2};
+  for (const void* q : src)
+    if (q == nullptr || misaligned(q)) return BPT_ERR_INVALID_ARG;
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace_bytes < dp.total) return BPT_ERR_WORKSPACE;
+  const int64_t n[6] = {d * d, d * d, d * d, d * d, d * d_ff, d_ff * d};
+  const Span sw(workspace, dp.total);
+  for (int k = 0; k < 6; ++k)
+    if (sw.overlaps(Span(src[k], size_t(n[k]) * 2))) return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != BPT_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (cudaMemsetAsync(ws, 0, kHeaderBytes, s) != cudaSuccess ||
+      cudaMemsetAsync(ws + dp.off_attn, 0, dp.attn_bytes, s) != cudaSuccess)
+    return BPT_ERR_CUDA;
+  bpt::CvtSegments cs{};
+  __half* dst = reinterpret_cast<__half*>(ws + dp.P.off_w16);
+  long long acc = 0;
+  for (int k = 0; k < 6; ++k) {
+    cs.src[k] = static_cast<const __nv_bfloat16*>(src[k]);
+    cs.dst[k] = dst;
+    dst += n[k];
+    acc += n[k] / 8;
+    cs.n8_end[k] = acc;
+  }
+  cs.count = 6;
+  const unsigned grid = unsigned(std::min<long long>((acc + 255) / 256, int64_t(sms) * 8));
+  bpt::cvt_bf16_to_f16_kernel<<<grid, 256, 0, s>>>(cs, reinterpret_cast<uint32_t*>(ws));
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status bpt_layer_decode(const void* x, const void* ln1, const void* ln2, const void* b_1,
+                            const void* b_2, const bpt_cache* cache, int64_t d, int64_t d_ff,
+                            int64_t window, int64_t sinks, float* acc, int32_t* pos,
+                            const int32_t* seen, int32_t* new_lens, float* out, void* workspace,
+                            size_t workspace_bytes, bpt_stream_t stream) {
+  DecodePlan dp;
+  bpt_status st = decode_plan(cache, d, d_ff, acc != nullptr, &dp);
+  if (st != BPT_OK) return st;
+  if (window < 0 || sinks < 0) return BPT_ERR_INVALID_ARG;
+  if (cache->batch == 0) return BPT_OK;
+  for (const void* q : {x, ln1, ln2, b_1, b_2, static_cast<const void*>(out),
+                        static_cast<const void*>(workspace)})
+    if (q == nullptr || misaligned(q)) return BPT_ERR_INVALID_ARG;
+  if (new_lens == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace_bytes < dp.total) return BPT_ERR_WORKSPACE;
+  const int64_t B = cache->batch;
+  const Span sw(workspace, dp.total), so(out, size_t(B * d) * 4);
+  if (so.overlaps(sw)) return BPT_ERR_INVALID_ARG;
+  const size_t rows = size_t(cache->pages) * size_t(cache->kv_heads * cache->page_size) *
+                      size_t(cache->d_k) * 2;
+  const size_t slots = size_t(B * cache->kv_heads) * size_t(cache->max_pages * cache->page_size) * 4;
+  const Span others[] = {Span(x, size_t(B * d) * 2),      Span(ln1, size_t(2 * d) * 2),
+                         Span(ln2, size_t(2 * d) * 2),    Span(b_1, size_t(d_ff) * 2),
+                         Span(b_2, size_t(d) * 2),        Span(cache->k, rows),
+                         Span(cache->v, rows),            Span(cache->lens, size_t(B) * 4),
+                         Span(new_lens, size_t(B) * 4),
+                         Span(cache->page_table, size_t(B * cache->max_pages) * 4),
+                         Span(acc, acc ? slots : 0),      Span(pos, pos ? slots : 0),
+                         Span(seen, seen ? size_t(B) * 4 : 0)};
+  for (const Span& o : others)
+    if (so.overlaps(o) || sw.overlaps(o)) return BPT_ERR_INVALID_ARG;
+  // the append writes the cache, new_lens, acc and pos while x and the
+  // parameters (the first five) are still to be read
+  for (int i = 0; i < 5; ++i)
+    for (int j : {5, 6, 8, 10, 11})
+      if (others[i].overlaps(others[j])) return BPT_ERR_INVALID_ARG;
+  {
+    // everything the append and the attention would refuse
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    const __half* q = reinterpret_cast<const __half*>(w + dp.P.off_qkv);
+    const int64_t dk = dp.P.dk, st6[6] = {3 * d, 3 * d, dk, 3 * d, 3 * d, dk};
+    st = bpt_host::cache_append(cache, q + d, q + 2 * d, 1, st6, nullptr, new_lens, acc, pos, seen,
+                                w, kHeaderBytes, stream, nullptr, true);
+    if (st != BPT_OK) return st;
+    st = bpt_host::attn_decode(cache, q, dp.P.h, 3 * d, dk, window, sinks, acc, acc,
+                               w + dp.P.off_o, d, dk, w + dp.off_attn, dp.attn_bytes, stream,
+                               nullptr, true);
+    if (st != BPT_OK) return st;
+  }
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != BPT_OK) return st;
+  st = get_encoder();
+  if (st != BPT_OK) return st;
+  AttnForm form{};
+  form.decode = true;
+  form.window = window;
+  form.sinks = sinks;
+  form.cache = cache;
+  form.new_lens = new_lens;
+  form.acc = acc;
+  form.pos = pos;
+  form.seen = seen;
+  form.ws = static_cast<uint8_t*>(workspace) + dp.off_attn;
+  form.ws_bytes = dp.attn_bytes;
+  // (the weights' pointers are only read by their conversion, which was done)
+  return forward_bf16(dp.P, x, ln1, nullptr, nullptr, nullptr, nullptr, ln2, nullptr, b_1, nullptr,
+                      b_2, out, nullptr, static_cast<uint8_t*>(workspace),
+                      reinterpret_cast<cudaStream_t>(stream), sms, nullptr, nullptr, nullptr,
+                      &form);
 }
 
 bpt_status bpt_read_device_error(void* workspace, bpt_stream_t stream, uint32_t* site) {

@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "bpt.h"
+#include "ops_internal.h"
 
 // The shared device helpers define functions in namespace bpt; in this unit
 // the namespace gets its own name, so that both units link into one library.
@@ -144,7 +145,7 @@ size_t cache_bytes(const bpt_cache* c) {
 size_t slots_bytes(const bpt_cache* c) {  // [batch][kv_heads][max_pages * page_size] words
   return size_t(c->batch) * size_t(c->kv_heads) * size_t(c->max_pages * c->page_size) * 4;
 }
-bpt::CacheView view_of(const bpt_cache* c, void* ws) {
+bpt::CacheView view_of(const bpt_cache* c, uint32_t* err) {
   bpt::CacheView v{};
   v.k = static_cast<uint4*>(c->k);
   v.v = static_cast<uint4*>(c->v);
@@ -163,7 +164,7 @@ bpt::CacheView view_of(const bpt_cache* c, void* ws) {
     v.ps_mul = uint32_t(((uint64_t(1) << (31 + l)) + v.ps - 1) / v.ps);
     v.ps_shift = uint32_t(l - 1);
   }
-  v.err = static_cast<uint32_t*>(ws);
+  v.err = err;
   return v;
 }
 uint32_t clamp_u31(int64_t v) { return uint32_t(std::min<int64_t>(v, 0x7FFFFFFF)); }
@@ -382,20 +383,14 @@ cudaError_t launch_window_bwd(const CUtensorMap& q, const CUtensorMap& k, const 
 
 }  // namespace
 
-extern "C" {
+namespace bpt_host {
 
-bpt_status bpt_cache_workspace_size(const bpt_cache* cache, size_t* bytes) {
-  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
-  const bpt_status st = check_cache(cache);
-  if (st != BPT_OK) return st;
-  *bytes = cache_layout(cache).total;
-  return BPT_OK;
-}
-
-bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const void* v_new,
+bpt_status cache_append(const bpt_cache* cache, const void* k_new, const void* v_new,
                             int64_t tokens, const int64_t* strides, const int32_t* counts,
                             int32_t* new_lens, float* acc, int32_t* pos, const int32_t* seen,
-                            void* workspace, size_t workspace_bytes, bpt_stream_t stream) {
+                            void* workspace, size_t workspace_bytes, bpt_stream_t stream, uint32_t* err,
+                         bool check_only) {
+  if (err == nullptr) err = static_cast<uint32_t*>(workspace);
   bpt_status st = check_cache(cache);
   if (st != BPT_OK) return st;
   if (tokens < 0) return BPT_ERR_INVALID_ARG;
@@ -430,11 +425,12 @@ bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const voi
       any_meets(ra, {ik, iv, rl, rt, rp, rc, rs, rw}) ||
       any_meets(rp, {ik, iv, rl, rt, rc, rs, rw}) || any_meets(rw, {ik, iv, rl, rt, rc, rs}))
     return BPT_ERR_INVALID_ARG;
+  if (check_only) return BPT_OK;
   int sms = 0;
   st = ops_device(&sms);
   if (st != BPT_OK) return st;
   bpt::AppendParams p{};
-  p.c = view_of(cache, workspace);
+  p.c = view_of(cache, err);
   p.k = static_cast<const uint4*>(k_new);
   p.v = static_cast<const uint4*>(v_new);
   p.k_b = strides[0] / 8;
@@ -455,6 +451,271 @@ bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const voi
   bpt::cache_append_kernel<<<dim3(unsigned(blocks), unsigned(B)), bpt::kAppendThreads, 0,
                              reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
+                           int64_t q_stride_b, int64_t q_stride_h, int64_t window, int64_t sinks,
+                           const float* acc, float* acc_out, void* out, int64_t out_stride_b,
+                           int64_t out_stride_h, void* workspace, size_t workspace_bytes,
+                           bpt_stream_t stream, uint32_t* err,
+                         bool check_only) {
+  if (err == nullptr) err = static_cast<uint32_t*>(workspace);
+  bpt_status st = check_cache(cache);
+  if (st != BPT_OK) return st;
+  if (window < 0 || sinks < 0 || (acc == nullptr) != (acc_out == nullptr))
+    return BPT_ERR_INVALID_ARG;
+  DecodeLayout l;
+  st = decode_layout(cache, heads, acc != nullptr, &l);
+  if (st != BPT_OK) return st;
+  if (cache->batch == 0) return BPT_OK;
+  st = check_cache_pointers(cache);
+  if (st != BPT_OK) return st;
+  const int64_t B = cache->batch, dk = cache->d_k;
+  for (const void* p : {q, static_cast<const void*>(out)})
+    if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
+  for (int64_t x : {q_stride_b, q_stride_h, out_stride_b, out_stride_h})
+    if (x < 0 || x % 8 != 0) return BPT_ERR_INVALID_ARG;
+  // output rows must not meet one another
+  if ((heads > 1 && out_stride_h < dk) || (B > 1 && out_stride_b < dk) ||
+      (B > 1 && heads > 1 && out_stride_b < (heads - 1) * out_stride_h + dk &&
+       out_stride_h < (B - 1) * out_stride_b + dk))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace == nullptr || unaligned(workspace, 256) || unaligned(acc, 4) ||
+      unaligned(acc_out, 4))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace_bytes < l.total) return BPT_ERR_WORKSPACE;
+  const Range rk(cache->k, cache_bytes(cache)), rv(cache->v, cache_bytes(cache)),
+      rl(cache->lens, size_t(B) * 4), rt(cache->page_table, size_t(B * cache->max_pages) * 4),
+      ra(acc, acc ? slots_bytes(cache) : 0), rao(acc_out, acc ? slots_bytes(cache) : 0),
+      rq(q, extent({{B, q_stride_b}, {heads, q_stride_h}}, dk)),
+      ro(out, extent({{B, out_stride_b}, {heads, out_stride_h}}, dk)), rw(workspace, l.total);
+  // acc may be updated in place; nothing else that is written meets another array
+  if ((acc_out != acc && rao.meets(ra)) || any_meets(rao, {rk, rv, rl, rt, rq, ro, rw}) ||
+      any_meets(ro, {rk, rv, rl, rt, rq, ra, rw}) || any_meets(rw, {rk, rv, rl, rt, rq, ra}))
+    return BPT_ERR_INVALID_ARG;
+  if (check_only) return BPT_OK;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  bpt::DecodeParams p{};
+  p.c = view_of(cache, err);
+  p.q = q;
+  p.q_b = q_stride_b;
+  p.q_h = q_stride_h;
+  p.out = out;
+  p.o_b = out_stride_b;
+  p.o_h = out_stride_h;
+  p.B = uint32_t(B);
+  p.h = uint32_t(heads);
+  p.g = uint32_t(heads / cache->kv_heads);
+  p.chunks = uint32_t(l.chunks);
+  p.rows = uint32_t(l.rows);
+  p.scores_ld = scores_ld(cache);
+  p.window = clamp_u31(window);
+  p.sinks = clamp_u31(sinks);
+  p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
+  p.count = reinterpret_cast<uint32_t*>(ws + l.off_count);
+  p.part_o = reinterpret_cast<float*>(ws + l.off_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + l.off_ml);
+  p.seg_ml = reinterpret_cast<float2*>(ws + l.off_seg);
+  const int per_sm = l.rows == 16 ? bpt::DecodeShape<128, 2>::CTAS
+                     : dk == 128  ? bpt::DecodeShape<128, 1>::CTAS
+                                  : bpt::DecodeShape<64, 1>::CTAS;
+  p.ctas = uint32_t(per_sm * std::min(sms, bpt::kDecodeMaxSms));
+  p.scores = acc != nullptr ? reinterpret_cast<float*>(ws + l.off_scores) : nullptr;
+  p.acc = acc;
+  p.acc_out = acc_out;
+  const unsigned slot_blocks =
+      acc != nullptr ? unsigned((p.c.cap + bpt::kWeightSlots - 1) / bpt::kWeightSlots) : 0u;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cache->dtype == BPT_BF16)
+    e = dk == 128 ? launch_decode<__nv_bfloat16, 128>(p, slot_blocks, s)
+                  : launch_decode<__nv_bfloat16, 64>(p, slot_blocks, s);
+  else
+    e = dk == 128 ? launch_decode<__half, 128>(p, slot_blocks, s)
+                  : launch_decode<__half, 64>(p, slot_blocks, s);
+  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status window_forward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
+                                   const bpt_rows* v, const int32_t* lens, const bpt_rows* out,
+                                   float* stats, void* workspace, size_t workspace_bytes,
+                                   bpt_stream_t stream, uint32_t* err) {
+  if (err == nullptr) err = static_cast<uint32_t*>(workspace);
+  bpt_status st = check_window(w);
+  if (st != BPT_OK) return st;
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr) return BPT_ERR_INVALID_ARG;
+  if (w->batch == 0 || w->n_q == 0) return BPT_OK;
+  const int64_t B = w->batch, nq = w->n_q, nkv = w->n_kv, h = w->heads, hkv = w->kv_heads,
+                dk = w->d_k;
+  if (!rows_ok(*q, B, nq, h) || !rows_ok(*k, B, nkv, hkv) || !rows_ok(*v, B, nkv, hkv) ||
+      !rows_ok(*out, B, nq, h) || !rows_apart(*out, B, nq, h, dk) || unaligned(lens, 4) ||
+      unaligned(stats, 8) || workspace == nullptr || unaligned(workspace, 256))
+    return BPT_ERR_INVALID_ARG;
+  if (workspace_bytes < kOpsHeader) return BPT_ERR_WORKSPACE;
+  const Range rq = rows_range(*q, B, nq, h, dk), rk = rows_range(*k, B, nkv, hkv, dk),
+              rv = rows_range(*v, B, nkv, hkv, dk), rl(lens, size_t(B) * 4),
+              rs(stats, size_t(B * h) * size_t(nq) * 8), rw(workspace, kOpsHeader);
+  const Range ro = rows_range(*out, B, nq, h, dk);
+  if (any_meets(ro, {rq, rk, rv, rl, rs, rw}) || any_meets(rs, {rq, rk, rv, rl, rw}) ||
+      any_meets(rw, {rq, rk, rv, rl}))
+    return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  st = ops_encoder();
+  if (st != BPT_OK) return st;
+  CUtensorMap mq, mk, mv;
+  if (!map_rows(&mq, *q, B, nq, h, dk) || !map_rows(&mk, *k, B, nkv, hkv, dk) ||
+      !map_rows(&mv, *v, B, nkv, hkv, dk))
+    return BPT_ERR_CUDA;
+  bpt::WindowParams p{};
+  p.nq = int(nq);
+  p.nkv = int(nkv);
+  p.h = int(h);
+  p.hkv = int(hkv);
+  p.g = int(h / hkv);
+  p.units = int((nq + 127) / 128) * p.g;
+  p.npairs = (p.units + 1) / 2;
+  p.window = int(std::min<int64_t>(w->window, nkv));
+  p.sinks = int(std::min<int64_t>(w->sinks, nkv));
+  p.lens = lens;
+  p.q = q->data;
+  p.k = k->data;
+  p.v = v->data;
+  p.q_b = q->stride_b; p.q_n = q->stride_n; p.q_h = q->stride_h;
+  p.k_b = k->stride_b; p.k_n = k->stride_n; p.k_h = k->stride_h;
+  p.v_b = v->stride_b; p.v_n = v->stride_n; p.v_h = v->stride_h;
+  p.o = out->data;
+  p.o_b = out->stride_b; p.o_n = out->stride_n; p.o_h = out->stride_h;
+  p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
+  p.stats = reinterpret_cast<float2*>(stats);
+  p.err = err;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (w->dtype == BPT_BF16)
+    e = dk == 128 ? launch_window<__nv_bfloat16, 128>(mq, mk, mv, p, B, s)
+                  : launch_window<__nv_bfloat16, 64>(mq, mk, mv, p, B, s);
+  else
+    e = dk == 128 ? launch_window<__half, 128>(mq, mk, mv, p, B, s)
+                  : launch_window<__half, 64>(mq, mk, mv, p, B, s);
+  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+bpt_status window_backward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
+                                    const bpt_rows* v, const bpt_rows* o, const float* stats,
+                                    const bpt_rows* d_o, const int32_t* lens, const bpt_rows* dq,
+                                    const bpt_rows* dk, const bpt_rows* dv, void* workspace,
+                                    size_t workspace_bytes, bpt_stream_t stream, uint32_t* err) {
+  if (err == nullptr) err = static_cast<uint32_t*>(workspace);
+  bpt_status st = check_window_bwd(w);
+  if (st != BPT_OK) return st;
+  for (const bpt_rows* r : {q, k, v, o, d_o, dq, dk, dv})
+    if (r == nullptr) return BPT_ERR_INVALID_ARG;
+  const int64_t B = w->batch, nq = w->n_q, nkv = w->n_kv, h = w->heads, hkv = w->kv_heads,
+                c = w->d_k;
+  // (with keys but without queries the gradients of the keys are zeros: the
+  // call would be of no use and is refused)
+  if (B == 0 || nkv == 0) return BPT_OK;
+  if (nq == 0) return BPT_ERR_INVALID_ARG;
+  if (!rows_ok(*q, B, nq, h) || !rows_ok(*k, B, nkv, hkv) || !rows_ok(*v, B, nkv, hkv) ||
+      !rows_ok(*o, B, nq, h) || !rows_ok(*d_o, B, nq, h) || !rows_ok(*dq, B, nq, h) ||
+      !rows_ok(*dk, B, nkv, hkv) || !rows_ok(*dv, B, nkv, hkv) ||
+      !rows_apart(*dq, B, nq, h, c) || !rows_apart(*dk, B, nkv, hkv, c) ||
+      !rows_apart(*dv, B, nkv, hkv, c) || stats == nullptr || unaligned(stats, 8) ||
+      unaligned(lens, 4) || workspace == nullptr || unaligned(workspace, 256))
+    return BPT_ERR_INVALID_ARG;
+  const WindowBwdPlan plan = window_bwd_plan(w);
+  if (workspace_bytes < plan.total) return BPT_ERR_WORKSPACE;
+  const Range rq = rows_range(*q, B, nq, h, c), rk = rows_range(*k, B, nkv, hkv, c),
+              rv = rows_range(*v, B, nkv, hkv, c), ro = rows_range(*o, B, nq, h, c),
+              rd = rows_range(*d_o, B, nq, h, c), rl(lens, size_t(B) * 4),
+              rs(stats, size_t(B * h) * size_t(nq) * 8), rw(workspace, plan.total);
+  // Gradients may interleave with one another (the parts of one packed
+  // gradient), not with what is read.
+  for (const Range& r : {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
+                         rows_range(*dv, B, nkv, hkv, c), rw})
+    if (any_meets(r, {rq, rk, rv, ro, rd, rl, rs})) return BPT_ERR_INVALID_ARG;
+  if (any_meets(rw, {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
+                     rows_range(*dv, B, nkv, hkv, c)}) ||
+      dq->data == dk->data || dq->data == dv->data || dk->data == dv->data)
+    return BPT_ERR_INVALID_ARG;
+  int sms = 0;
+  st = ops_device(&sms);
+  if (st != BPT_OK) return st;
+  st = ops_encoder();
+  if (st != BPT_OK) return st;
+  CUtensorMap mq, mk, mv, md;
+  if (!map_rows(&mq, *q, B, nq, h, c) || !map_rows(&mk, *k, B, nkv, hkv, c) ||
+      !map_rows(&mv, *v, B, nkv, hkv, c) || !map_rows(&md, *d_o, B, nq, h, c))
+    return BPT_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* amax = nullptr;
+  if (w->dtype == BPT_F16) {
+    amax = reinterpret_cast<uint32_t*>(ws + kAmaxOffset);
+    if (cudaMemsetAsync(amax, 0, 4, s) != cudaSuccess) return BPT_ERR_CUDA;
+  }
+  bpt::WindowTermsParams tp{};
+  tp.o = o->data;
+  tp.o_b = o->stride_b; tp.o_n = o->stride_n; tp.o_h = o->stride_h;
+  tp.d_o = d_o->data;
+  tp.d_b = d_o->stride_b; tp.d_n = d_o->stride_n; tp.d_h = d_o->stride_h;
+  tp.stats = reinterpret_cast<const float2*>(stats);
+  tp.terms = reinterpret_cast<float2*>(ws + plan.off_terms);
+  tp.amax = amax;
+  tp.lens = lens;
+  tp.B = int(B); tp.nq = int(nq); tp.nkv = int(nkv); tp.h = int(h);
+  tp.err = err;
+  bpt::WindowBwdParams p{};
+  p.nq = int(nq); p.nkv = int(nkv); p.h = int(h); p.hkv = int(hkv); p.g = int(h / hkv);
+  p.nqb = int((nq + 127) / 128); p.nblk = int((nkv + 127) / 128);
+  p.window = int(std::min<int64_t>(w->window, nkv));
+  p.sinks = int(std::min<int64_t>(w->sinks, nkv));
+  p.lens = lens;
+  p.terms = tp.terms;
+  p.amax = amax;
+  p.dq = dq->data;
+  p.dq_b = dq->stride_b; p.dq_n = dq->stride_n; p.dq_h = dq->stride_h;
+  p.dk = dk->data;
+  p.dk_b = dk->stride_b; p.dk_n = dk->stride_n; p.dk_h = dk->stride_h;
+  p.dv = dv->data;
+  p.dv_b = dv->stride_b; p.dv_n = dv->stride_n; p.dv_h = dv->stride_h;
+  p.scale = float(1.0 / std::sqrt(double(c)));
+  p.part_len = plan.part_len;
+  p.split_parts = int(plan.cut_parts);
+  p.part = reinterpret_cast<float*>(ws + plan.off_part);
+  p.err = tp.err;
+  cudaError_t e;
+  using bf = __nv_bfloat16;
+  if (w->dtype == BPT_BF16)
+    e = c == 128 ? launch_window_bwd<bf, 128>(mq, mk, mv, md, tp, p, plan, B, s)
+                 : launch_window_bwd<bf, 64>(mq, mk, mv, md, tp, p, plan, B, s);
+  else
+    e = c == 128 ? launch_window_bwd<__half, 128>(mq, mk, mv, md, tp, p, plan, B, s)
+                 : launch_window_bwd<__half, 64>(mq, mk, mv, md, tp, p, plan, B, s);
+  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+}  // namespace bpt_host
+
+extern "C" {
+
+bpt_status bpt_cache_workspace_size(const bpt_cache* cache, size_t* bytes) {
+  if (bytes == nullptr) return BPT_ERR_INVALID_ARG;
+  const bpt_status st = check_cache(cache);
+  if (st != BPT_OK) return st;
+  *bytes = cache_layout(cache).total;
+  return BPT_OK;
+}
+
+bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const void* v_new,
+                            int64_t tokens, const int64_t* strides, const int32_t* counts,
+                            int32_t* new_lens, float* acc, int32_t* pos, const int32_t* seen,
+                            void* workspace, size_t workspace_bytes, bpt_stream_t stream) {
+  return bpt_host::cache_append(cache, k_new, v_new, tokens, strides, counts, new_lens, acc, pos, seen, workspace, workspace_bytes, stream, nullptr);
 }
 
 bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recent, int64_t sinks,
@@ -494,7 +755,7 @@ bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recen
   if (st != BPT_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   bpt::EvictParams p{};
-  p.c = view_of(cache, workspace);
+  p.c = view_of(cache, static_cast<uint32_t*>(workspace));
   p.acc = acc;
   p.pos = pos;
   p.seen = seen;
@@ -565,82 +826,7 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
                            const float* acc, float* acc_out, void* out, int64_t out_stride_b,
                            int64_t out_stride_h, void* workspace, size_t workspace_bytes,
                            bpt_stream_t stream) {
-  bpt_status st = check_cache(cache);
-  if (st != BPT_OK) return st;
-  if (window < 0 || sinks < 0 || (acc == nullptr) != (acc_out == nullptr))
-    return BPT_ERR_INVALID_ARG;
-  DecodeLayout l;
-  st = decode_layout(cache, heads, acc != nullptr, &l);
-  if (st != BPT_OK) return st;
-  if (cache->batch == 0) return BPT_OK;
-  st = check_cache_pointers(cache);
-  if (st != BPT_OK) return st;
-  const int64_t B = cache->batch, dk = cache->d_k;
-  for (const void* p : {q, static_cast<const void*>(out)})
-    if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
-  for (int64_t x : {q_stride_b, q_stride_h, out_stride_b, out_stride_h})
-    if (x < 0 || x % 8 != 0) return BPT_ERR_INVALID_ARG;
-  // output rows must not meet one another
-  if ((heads > 1 && out_stride_h < dk) || (B > 1 && out_stride_b < dk) ||
-      (B > 1 && heads > 1 && out_stride_b < (heads - 1) * out_stride_h + dk &&
-       out_stride_h < (B - 1) * out_stride_b + dk))
-    return BPT_ERR_INVALID_ARG;
-  if (workspace == nullptr || unaligned(workspace, 256) || unaligned(acc, 4) ||
-      unaligned(acc_out, 4))
-    return BPT_ERR_INVALID_ARG;
-  if (workspace_bytes < l.total) return BPT_ERR_WORKSPACE;
-  const Range rk(cache->k, cache_bytes(cache)), rv(cache->v, cache_bytes(cache)),
-      rl(cache->lens, size_t(B) * 4), rt(cache->page_table, size_t(B * cache->max_pages) * 4),
-      ra(acc, acc ? slots_bytes(cache) : 0), rao(acc_out, acc ? slots_bytes(cache) : 0),
-      rq(q, extent({{B, q_stride_b}, {heads, q_stride_h}}, dk)),
-      ro(out, extent({{B, out_stride_b}, {heads, out_stride_h}}, dk)), rw(workspace, l.total);
-  // acc may be updated in place; nothing else that is written meets another array
-  if ((acc_out != acc && rao.meets(ra)) || any_meets(rao, {rk, rv, rl, rt, rq, ro, rw}) ||
-      any_meets(ro, {rk, rv, rl, rt, rq, ra, rw}) || any_meets(rw, {rk, rv, rl, rt, rq, ra}))
-    return BPT_ERR_INVALID_ARG;
-  int sms = 0;
-  st = ops_device(&sms);
-  if (st != BPT_OK) return st;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  bpt::DecodeParams p{};
-  p.c = view_of(cache, workspace);
-  p.q = q;
-  p.q_b = q_stride_b;
-  p.q_h = q_stride_h;
-  p.out = out;
-  p.o_b = out_stride_b;
-  p.o_h = out_stride_h;
-  p.B = uint32_t(B);
-  p.h = uint32_t(heads);
-  p.g = uint32_t(heads / cache->kv_heads);
-  p.chunks = uint32_t(l.chunks);
-  p.rows = uint32_t(l.rows);
-  p.scores_ld = scores_ld(cache);
-  p.window = clamp_u31(window);
-  p.sinks = clamp_u31(sinks);
-  p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
-  p.count = reinterpret_cast<uint32_t*>(ws + l.off_count);
-  p.part_o = reinterpret_cast<float*>(ws + l.off_o);
-  p.part_ml = reinterpret_cast<float2*>(ws + l.off_ml);
-  p.seg_ml = reinterpret_cast<float2*>(ws + l.off_seg);
-  const int per_sm = l.rows == 16 ? bpt::DecodeShape<128, 2>::CTAS
-                     : dk == 128  ? bpt::DecodeShape<128, 1>::CTAS
-                                  : bpt::DecodeShape<64, 1>::CTAS;
-  p.ctas = uint32_t(per_sm * std::min(sms, bpt::kDecodeMaxSms));
-  p.scores = acc != nullptr ? reinterpret_cast<float*>(ws + l.off_scores) : nullptr;
-  p.acc = acc;
-  p.acc_out = acc_out;
-  const unsigned slot_blocks =
-      acc != nullptr ? unsigned((p.c.cap + bpt::kWeightSlots - 1) / bpt::kWeightSlots) : 0u;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (cache->dtype == BPT_BF16)
-    e = dk == 128 ? launch_decode<__nv_bfloat16, 128>(p, slot_blocks, s)
-                  : launch_decode<__nv_bfloat16, 64>(p, slot_blocks, s);
-  else
-    e = dk == 128 ? launch_decode<__half, 128>(p, slot_blocks, s)
-                  : launch_decode<__half, 64>(p, slot_blocks, s);
-  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return bpt_host::attn_decode(cache, q, heads, q_stride_b, q_stride_h, window, sinks, acc, acc_out, out, out_stride_b, out_stride_h, workspace, workspace_bytes, stream, nullptr);
 }
 
 bpt_status bpt_attn_window_workspace_size(const bpt_window* w, size_t* bytes) {
@@ -655,64 +841,7 @@ bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const
                                    const bpt_rows* v, const int32_t* lens, const bpt_rows* out,
                                    float* stats, void* workspace, size_t workspace_bytes,
                                    bpt_stream_t stream) {
-  bpt_status st = check_window(w);
-  if (st != BPT_OK) return st;
-  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr) return BPT_ERR_INVALID_ARG;
-  if (w->batch == 0 || w->n_q == 0) return BPT_OK;
-  const int64_t B = w->batch, nq = w->n_q, nkv = w->n_kv, h = w->heads, hkv = w->kv_heads,
-                dk = w->d_k;
-  if (!rows_ok(*q, B, nq, h) || !rows_ok(*k, B, nkv, hkv) || !rows_ok(*v, B, nkv, hkv) ||
-      !rows_ok(*out, B, nq, h) || !rows_apart(*out, B, nq, h, dk) || unaligned(lens, 4) ||
-      unaligned(stats, 8) || workspace == nullptr || unaligned(workspace, 256))
-    return BPT_ERR_INVALID_ARG;
-  if (workspace_bytes < kOpsHeader) return BPT_ERR_WORKSPACE;
-  const Range rq = rows_range(*q, B, nq, h, dk), rk = rows_range(*k, B, nkv, hkv, dk),
-              rv = rows_range(*v, B, nkv, hkv, dk), rl(lens, size_t(B) * 4),
-              rs(stats, size_t(B * h) * size_t(nq) * 8), rw(workspace, kOpsHeader);
-  const Range ro = rows_range(*out, B, nq, h, dk);
-  if (any_meets(ro, {rq, rk, rv, rl, rs, rw}) || any_meets(rs, {rq, rk, rv, rl, rw}) ||
-      any_meets(rw, {rq, rk, rv, rl}))
-    return BPT_ERR_INVALID_ARG;
-  int sms = 0;
-  st = ops_device(&sms);
-  if (st != BPT_OK) return st;
-  st = ops_encoder();
-  if (st != BPT_OK) return st;
-  CUtensorMap mq, mk, mv;
-  if (!map_rows(&mq, *q, B, nq, h, dk) || !map_rows(&mk, *k, B, nkv, hkv, dk) ||
-      !map_rows(&mv, *v, B, nkv, hkv, dk))
-    return BPT_ERR_CUDA;
-  bpt::WindowParams p{};
-  p.nq = int(nq);
-  p.nkv = int(nkv);
-  p.h = int(h);
-  p.hkv = int(hkv);
-  p.g = int(h / hkv);
-  p.units = int((nq + 127) / 128) * p.g;
-  p.npairs = (p.units + 1) / 2;
-  p.window = int(std::min<int64_t>(w->window, nkv));
-  p.sinks = int(std::min<int64_t>(w->sinks, nkv));
-  p.lens = lens;
-  p.q = q->data;
-  p.k = k->data;
-  p.v = v->data;
-  p.q_b = q->stride_b; p.q_n = q->stride_n; p.q_h = q->stride_h;
-  p.k_b = k->stride_b; p.k_n = k->stride_n; p.k_h = k->stride_h;
-  p.v_b = v->stride_b; p.v_n = v->stride_n; p.v_h = v->stride_h;
-  p.o = out->data;
-  p.o_b = out->stride_b; p.o_n = out->stride_n; p.o_h = out->stride_h;
-  p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
-  p.stats = reinterpret_cast<float2*>(stats);
-  p.err = static_cast<uint32_t*>(workspace);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (w->dtype == BPT_BF16)
-    e = dk == 128 ? launch_window<__nv_bfloat16, 128>(mq, mk, mv, p, B, s)
-                  : launch_window<__nv_bfloat16, 64>(mq, mk, mv, p, B, s);
-  else
-    e = dk == 128 ? launch_window<__half, 128>(mq, mk, mv, p, B, s)
-                  : launch_window<__half, 64>(mq, mk, mv, p, B, s);
-  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return bpt_host::window_forward(w, q, k, v, lens, out, stats, workspace, workspace_bytes, stream, nullptr);
 }
 
 bpt_status bpt_attn_window_backward_workspace_size(const bpt_window* w, size_t* bytes) {
@@ -728,93 +857,7 @@ bpt_status bpt_attn_window_backward(const bpt_window* w, const bpt_rows* q, cons
                                     const bpt_rows* d_o, const int32_t* lens, const bpt_rows* dq,
                                     const bpt_rows* dk, const bpt_rows* dv, void* workspace,
                                     size_t workspace_bytes, bpt_stream_t stream) {
-  bpt_status st = check_window_bwd(w);
-  if (st != BPT_OK) return st;
-  for (const bpt_rows* r : {q, k, v, o, d_o, dq, dk, dv})
-    if (r == nullptr) return BPT_ERR_INVALID_ARG;
-  const int64_t B = w->batch, nq = w->n_q, nkv = w->n_kv, h = w->heads, hkv = w->kv_heads,
-                c = w->d_k;
-  // (with keys but without queries the gradients of the keys are zeros: the
-  // call would be of no use and is refused)
-  if (B == 0 || nkv == 0) return BPT_OK;
-  if (nq == 0) return BPT_ERR_INVALID_ARG;
-  if (!rows_ok(*q, B, nq, h) || !rows_ok(*k, B, nkv, hkv) || !rows_ok(*v, B, nkv, hkv) ||
-      !rows_ok(*o, B, nq, h) || !rows_ok(*d_o, B, nq, h) || !rows_ok(*dq, B, nq, h) ||
-      !rows_ok(*dk, B, nkv, hkv) || !rows_ok(*dv, B, nkv, hkv) ||
-      !rows_apart(*dq, B, nq, h, c) || !rows_apart(*dk, B, nkv, hkv, c) ||
-      !rows_apart(*dv, B, nkv, hkv, c) || stats == nullptr || unaligned(stats, 8) ||
-      unaligned(lens, 4) || workspace == nullptr || unaligned(workspace, 256))
-    return BPT_ERR_INVALID_ARG;
-  const WindowBwdPlan plan = window_bwd_plan(w);
-  if (workspace_bytes < plan.total) return BPT_ERR_WORKSPACE;
-  const Range rq = rows_range(*q, B, nq, h, c), rk = rows_range(*k, B, nkv, hkv, c),
-              rv = rows_range(*v, B, nkv, hkv, c), ro = rows_range(*o, B, nq, h, c),
-              rd = rows_range(*d_o, B, nq, h, c), rl(lens, size_t(B) * 4),
-              rs(stats, size_t(B * h) * size_t(nq) * 8), rw(workspace, plan.total);
-  // Gradients may interleave with one another (the parts of one packed
-  // gradient), not with what is read.
-  for (const Range& r : {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
-                         rows_range(*dv, B, nkv, hkv, c), rw})
-    if (any_meets(r, {rq, rk, rv, ro, rd, rl, rs})) return BPT_ERR_INVALID_ARG;
-  if (any_meets(rw, {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
-                     rows_range(*dv, B, nkv, hkv, c)}) ||
-      dq->data == dk->data || dq->data == dv->data || dk->data == dv->data)
-    return BPT_ERR_INVALID_ARG;
-  int sms = 0;
-  st = ops_device(&sms);
-  if (st != BPT_OK) return st;
-  st = ops_encoder();
-  if (st != BPT_OK) return st;
-  CUtensorMap mq, mk, mv, md;
-  if (!map_rows(&mq, *q, B, nq, h, c) || !map_rows(&mk, *k, B, nkv, hkv, c) ||
-      !map_rows(&mv, *v, B, nkv, hkv, c) || !map_rows(&md, *d_o, B, nq, h, c))
-    return BPT_ERR_CUDA;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint32_t* amax = nullptr;
-  if (w->dtype == BPT_F16) {
-    amax = reinterpret_cast<uint32_t*>(ws + kAmaxOffset);
-    if (cudaMemsetAsync(amax, 0, 4, s) != cudaSuccess) return BPT_ERR_CUDA;
-  }
-  bpt::WindowTermsParams tp{};
-  tp.o = o->data;
-  tp.o_b = o->stride_b; tp.o_n = o->stride_n; tp.o_h = o->stride_h;
-  tp.d_o = d_o->data;
-  tp.d_b = d_o->stride_b; tp.d_n = d_o->stride_n; tp.d_h = d_o->stride_h;
-  tp.stats = reinterpret_cast<const float2*>(stats);
-  tp.terms = reinterpret_cast<float2*>(ws + plan.off_terms);
-  tp.amax = amax;
-  tp.lens = lens;
-  tp.B = int(B); tp.nq = int(nq); tp.nkv = int(nkv); tp.h = int(h);
-  tp.err = reinterpret_cast<uint32_t*>(ws);
-  bpt::WindowBwdParams p{};
-  p.nq = int(nq); p.nkv = int(nkv); p.h = int(h); p.hkv = int(hkv); p.g = int(h / hkv);
-  p.nqb = int((nq + 127) / 128); p.nblk = int((nkv + 127) / 128);
-  p.window = int(std::min<int64_t>(w->window, nkv));
-  p.sinks = int(std::min<int64_t>(w->sinks, nkv));
-  p.lens = lens;
-  p.terms = tp.terms;
-  p.amax = amax;
-  p.dq = dq->data;
-  p.dq_b = dq->stride_b; p.dq_n = dq->stride_n; p.dq_h = dq->stride_h;
-  p.dk = dk->data;
-  p.dk_b = dk->stride_b; p.dk_n = dk->stride_n; p.dk_h = dk->stride_h;
-  p.dv = dv->data;
-  p.dv_b = dv->stride_b; p.dv_n = dv->stride_n; p.dv_h = dv->stride_h;
-  p.scale = float(1.0 / std::sqrt(double(c)));
-  p.part_len = plan.part_len;
-  p.split_parts = int(plan.cut_parts);
-  p.part = reinterpret_cast<float*>(ws + plan.off_part);
-  p.err = tp.err;
-  cudaError_t e;
-  using bf = __nv_bfloat16;
-  if (w->dtype == BPT_BF16)
-    e = c == 128 ? launch_window_bwd<bf, 128>(mq, mk, mv, md, tp, p, plan, B, s)
-                 : launch_window_bwd<bf, 64>(mq, mk, mv, md, tp, p, plan, B, s);
-  else
-    e = c == 128 ? launch_window_bwd<__half, 128>(mq, mk, mv, md, tp, p, plan, B, s)
-                 : launch_window_bwd<__half, 64>(mq, mk, mv, md, tp, p, plan, B, s);
-  return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return bpt_host::window_backward(w, q, k, v, o, stats, d_o, lens, dq, dk, dv, workspace, workspace_bytes, stream, nullptr);
 }
 
 }  // extern "C"

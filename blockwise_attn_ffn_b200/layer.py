@@ -11,6 +11,7 @@ import numpy as np
 import torch
 
 from . import _lib
+from .cache import cache_sizes, cache_struct, check, check_workspace, run, stream_of
 
 # Parameter tensors in C-ABI order, with their shapes in terms of (d, d_ff).
 PARAM_NAMES = ["ln1", "W_Q", "W_K", "W_V", "W_O", "ln2", "W_1", "b_1", "W_2", "b_2"]
@@ -243,3 +244,148 @@ def layer_backward(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, causal: 
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_layer_backward")
     return grads, workspace
+
+
+# --------------------------- the layer with a window and with a cache --
+def _layer_inputs(x, p):
+    """Checks x [B, N, d] and the parameters; returns their addresses."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, N, d]")
+    tensors = [x] + [p[k] for k in PARAM_NAMES]
+    for t in tensors:
+        if (not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype
+                or t.device != x.device):
+            raise ValueError("inputs must be contiguous tensors of one dtype on one GPU")
+    return [t.data_ptr() for t in tensors]
+
+
+def layer_forward_window(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, window: int,
+                         sinks: int = 0, lens: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None,
+                         stats: Optional[torch.Tensor] = None,
+                         keep_o: Optional[torch.Tensor] = None, cache=None,
+                         new_lens: Optional[torch.Tensor] = None,
+                         acc: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                         seen: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None):
+    """``layer_forward`` (bf16, causal) with sliding-window attention via
+    ``bpt_layer_forward_window``; returns (out, workspace).
+
+    stats [B, h, N, 2] fp32 and keep_o [B, N, d] fp16 receive what
+    ``layer_backward_window`` needs.  cache = (k_cache, v_cache, page_table,
+    lens): the tokens' K and V (lens[b] of them, if given) are appended, with
+    new_lens [B] int32 (required) and acc, pos, seen as for ``cache_append``."""
+    ptrs = _layer_inputs(x, p)
+    B, N, d = x.shape
+    d_ff = p["W_1"].shape[1]
+    code, index = _dtype_code(x), x.get_device()
+    if out is None:
+        out = torch.empty((B, N, d), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        st, nbytes = _lib.bpt_layer_forward_window_workspace_size(B, N, d, h, d_ff, code)
+        if st != _lib.BPT_OK:
+            raise _lib.BptError(st, "bpt_layer_forward_window_workspace_size")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    opt = lambda t, what, shape, dt: None if t is None else check(t, what, shape, dt, index)
+    c = None
+    slots = ()
+    if cache is not None:
+        c = cache_struct(*cache)
+        slots = (B, c.kv_heads, c.max_pages * c.page_size)
+    st = run(_lib.bpt_layer_forward_window, index, *ptrs, B, N, d, h, d_ff, code, window, sinks,
+             opt(lens, "lens", (B,), torch.int32), check(out, "out", (B, N, d), torch.float32, index),
+             opt(stats, "stats", (B, h, N, 2), torch.float32),
+             opt(keep_o, "keep_o", (B, N, d), torch.float16), c,
+             opt(new_lens, "new_lens", (B,), torch.int32), opt(acc, "acc", slots, torch.float32),
+             opt(pos, "pos", slots, torch.int32), opt(seen, "seen", (B,), torch.int32),
+             workspace.data_ptr(), workspace.numel(), stream_of(stream, index))
+    if st != _lib.BPT_OK:
+        raise _lib.BptError(st, "bpt_layer_forward_window")
+    return out, workspace
+
+
+def layer_backward_window(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, window: int,
+                          sinks: int, stats: torch.Tensor, o: torch.Tensor, dZ: torch.Tensor,
+                          lens: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of ``layer_forward_window`` via ``bpt_layer_backward_window``
+    (stats and o from it); returns (grads, workspace) as ``layer_backward``."""
+    ptrs = _layer_inputs(x, p)
+    B, N, d = x.shape
+    d_ff = p["W_1"].shape[1]
+    code, index = _dtype_code(x), x.get_device()
+    if workspace is None:
+        st, nbytes = _lib.bpt_layer_backward_window_workspace_size(B, N, d, h, d_ff, code, window,
+                                                                   sinks)
+        if st != _lib.BPT_OK:
+            raise _lib.BptError(st, "bpt_layer_backward_window_workspace_size")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    grads = {k: torch.empty(p[k].shape if k != "x" else x.shape, dtype=torch.float32,
+                            device=x.device) for k in GRAD_SHAPES}
+    st = run(_lib.bpt_layer_backward_window, index, *ptrs,
+             check(stats, "stats", (B, h, N, 2), torch.float32, index),
+             check(o, "o", (B, N, d), torch.float16, index),
+             check(dZ, "dZ", (B, N, d), torch.float32, index), B, N, d, h, d_ff, code, window,
+             sinks, None if lens is None else check(lens, "lens", (B,), torch.int32, index),
+             *[grads[k].data_ptr() for k in GRAD_SHAPES], workspace.data_ptr(), workspace.numel(),
+             stream_of(stream, index))
+    if st != _lib.BPT_OK:
+        raise _lib.BptError(st, "bpt_layer_backward_window")
+    return grads, workspace
+
+
+def layer_decode_workspace(p: Dict[str, torch.Tensor], k_cache: torch.Tensor,
+                           page_table: torch.Tensor, with_acc: bool = False,
+                           stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """A workspace for ``layer_decode`` steps with these weights (bf16) and a
+    cache of these sizes: ``bpt_layer_decode_prepare``, once."""
+    c = cache_sizes(k_cache, page_table)
+    d, d_ff = p["W_1"].shape
+    st, nbytes = _lib.bpt_layer_decode_workspace_size(c, d, d_ff, with_acc)
+    if st != _lib.BPT_OK:
+        raise _lib.BptError(st, "bpt_layer_decode_workspace_size")
+    index = k_cache.get_device()
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=k_cache.device)
+    shapes = dict(W_Q=(d, d), W_K=(d, d), W_V=(d, d), W_O=(d, d), W_1=(d, d_ff), W_2=(d_ff, d))
+    ptrs = [check(p[k], k, s, torch.bfloat16, index) for k, s in shapes.items()]
+    st = run(_lib.bpt_layer_decode_prepare, index, *ptrs, c, d, d_ff, with_acc,
+             workspace.data_ptr(), nbytes, stream_of(stream, index))
+    if st != _lib.BPT_OK:
+        raise _lib.BptError(st, "bpt_layer_decode_prepare")
+    return workspace
+
+
+def layer_decode(x: torch.Tensor, p: Dict[str, torch.Tensor], k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                 workspace: torch.Tensor, window: int = 0, sinks: int = 0,
+                 acc: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                 seen: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """The layer on one new token per sequence, x [B, d] bf16, over an fp16
+    cache via ``bpt_layer_decode``; returns (out [B, d] fp32, new_lens).  acc
+    is updated in place; new_lens is not the lens tensor: swap the two."""
+    c = cache_struct(k_cache, v_cache, page_table, lens)
+    index, B = k_cache.get_device(), lens.shape[0]
+    d, d_ff = p["W_1"].shape
+    bf = torch.bfloat16
+    slots = (B, c.kv_heads, c.max_pages * c.page_size)
+    if new_lens is None:
+        new_lens = torch.empty_like(lens)
+    if out is None:
+        out = torch.empty((B, d), dtype=torch.float32, device=x.device)
+    st = run(_lib.bpt_layer_decode, index, check(x, "x", (B, d), bf, index),
+             check(p["ln1"], "ln1", (2, d), bf, index), check(p["ln2"], "ln2", (2, d), bf, index),
+             check(p["b_1"], "b_1", (d_ff,), bf, index), check(p["b_2"], "b_2", (d,), bf, index), c,
+             d, d_ff, window, sinks,
+             None if acc is None else check(acc, "acc", slots, torch.float32, index),
+             None if pos is None else check(pos, "pos", slots, torch.int32, index),
+             None if seen is None else check(seen, "seen", (B,), torch.int32, index),
+             check(new_lens, "new_lens", (B,), torch.int32, index),
+             check(out, "out", (B, d), torch.float32, index),
+             check_workspace(workspace, index).data_ptr(), workspace.numel(),
+             stream_of(stream, index))
+    if st != _lib.BPT_OK:
+        raise _lib.BptError(st, "bpt_layer_decode")
+    return out, new_lens

@@ -773,6 +773,76 @@ bpt_status bpt_attn_window_backward(const bpt_window* w, const bpt_rows* q, cons
                                     const bpt_rows* dk, const bpt_rows* dv, void* workspace,
                                     size_t workspace_bytes, bpt_stream_t stream);
 
+/* ------------------------------- the layer with a window and with a cache --
+ * The BPT_BF16 layer with causal sliding-window attention (window, sinks and
+ * lens as for bpt_attn_window_forward; Q, K and V are the layer's fp16
+ * projection), its gradients, and its step for one new token per sequence
+ * over a paged cache (BPT_F16, kv_heads = h).  BPT_F32 layers are
+ * BPT_ERR_UNSUPPORTED.  Workspaces are 256-byte aligned.
+ *
+ * bpt_layer_forward_window -- Z of B sequences of N tokens; rows at positions
+ * >= lens[b] (lens nullable) get attention output 0 and are otherwise computed
+ * like the rest.  stats (nullable) [B, h, N, 2] and o (nullable, fp16 [B, N, d])
+ * receive what bpt_layer_backward_window reads.
+ * cache (nullable): the sequences' K and V are appended to it (a prompt's
+ * prefill: lens are the counts), with new_lens, acc, pos and seen as for
+ * bpt_cache_append.  Device errors as for bpt_layer_forward, and BPT_ERR_INDEX.
+ */
+bpt_status bpt_layer_forward_window_workspace_size(int64_t B, int64_t N, int64_t d, int64_t h,
+                                                   int64_t d_ff, bpt_dtype dtype, size_t* bytes);
+bpt_status bpt_layer_forward_window(const void* x, const void* ln1, const void* W_Q,
+                                    const void* W_K, const void* W_V, const void* W_O,
+                                    const void* ln2, const void* W_1, const void* b_1,
+                                    const void* W_2, const void* b_2, int64_t B, int64_t N,
+                                    int64_t d, int64_t h, int64_t d_ff, bpt_dtype dtype,
+                                    int64_t window, int64_t sinks, const int32_t* lens, float* out,
+                                    float* stats, void* o, const bpt_cache* cache,
+                                    int32_t* new_lens, float* acc, int32_t* pos,
+                                    const int32_t* seen, void* workspace, size_t workspace_bytes,
+                                    bpt_stream_t stream);
+
+/* bpt_layer_backward_window -- the gradients of bpt_layer_backward for the
+ * windowed layer; stats and o from bpt_layer_forward_window. */
+bpt_status bpt_layer_backward_window_workspace_size(int64_t B, int64_t N, int64_t d, int64_t h,
+                                                    int64_t d_ff, bpt_dtype dtype, int64_t window,
+                                                    int64_t sinks, size_t* bytes);
+bpt_status bpt_layer_backward_window(const void* x, const void* ln1, const void* W_Q,
+                                     const void* W_K, const void* W_V, const void* W_O,
+                                     const void* ln2, const void* W_1, const void* b_1,
+                                     const void* W_2, const void* b_2, const float* stats,
+                                     const void* o, const float* dZ, int64_t B, int64_t N,
+                                     int64_t d, int64_t h, int64_t d_ff, bpt_dtype dtype,
+                                     int64_t window, int64_t sinks, const int32_t* lens, float* dx,
+                                     float* d_ln1, float* dW_Q, float* dW_K, float* dW_V,
+                                     float* dW_O, float* d_ln2, float* dW_1, float* db_1,
+                                     float* dW_2, float* db_2, void* workspace,
+                                     size_t workspace_bytes, bpt_stream_t stream);
+
+/*
+ * bpt_layer_decode -- the layer on one new token per sequence: x [batch, d]
+ * bf16 -> out [batch, d] fp32.  The token's K and V are appended to the cache
+ * (new_lens = lens + 1; not the lens array; pos, seen nullable as for
+ * bpt_cache_append) and it attends over its sequence's slots (window, sinks,
+ * acc as for bpt_attn_decode, acc nullable and updated in place).
+ * bpt_layer_decode_prepare runs once per workspace and set of weights: it
+ * copies the weights to fp16 into the workspace and zeroes its counters; the
+ * steps then take the workspace as it is (the same cache sizes and with_acc).
+ * A step may be captured into a CUDA graph.  Device errors (BPT_ERR_INDEX
+ * among them) stay in the workspace until bpt_read_device_error.  Batches of
+ * more than 32768 sequences are BPT_ERR_UNSUPPORTED.
+ */
+bpt_status bpt_layer_decode_workspace_size(const bpt_cache* cache, int64_t d, int64_t d_ff,
+                                           int with_acc, size_t* bytes);
+bpt_status bpt_layer_decode_prepare(const void* W_Q, const void* W_K, const void* W_V,
+                                    const void* W_O, const void* W_1, const void* W_2,
+                                    const bpt_cache* cache, int64_t d, int64_t d_ff, int with_acc,
+                                    void* workspace, size_t workspace_bytes, bpt_stream_t stream);
+bpt_status bpt_layer_decode(const void* x, const void* ln1, const void* ln2, const void* b_1,
+                            const void* b_2, const bpt_cache* cache, int64_t d, int64_t d_ff,
+                            int64_t window, int64_t sinks, float* acc, int32_t* pos,
+                            const int32_t* seen, int32_t* new_lens, float* out, void* workspace,
+                            size_t workspace_bytes, bpt_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
