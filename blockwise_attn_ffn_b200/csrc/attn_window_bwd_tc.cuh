@@ -43,12 +43,23 @@
 
 namespace bpt {
 
-// Warps: TMA, UMMA, TMEM owner, row terms (dK/dV only); then 16 elementwise warps, four
-// per scheduler, each with 32 rows and 32 columns of a tile: with 8 warps of
-// 64 columns the phases took twice what the tensor cores need (two warps per
-// scheduler do not cover their own latencies).
-constexpr int kWinBwdElem = 512;
-constexpr int kWinBwdThreads = 128 + kWinBwdElem;
+// Tiles that stream through a block have kWinTile<D> rows: 128 queries or keys
+// at d_k = 128, where the accumulators leave room for one block per SM; 64 at
+// d_k = 64, so that two blocks share an SM (256 of its 512 tensor memory
+// columns each): with short windows a block has a few tiles only, and its own
+// chain of products and elementwise phases leaves most of the SM idle.
+template <int D>
+constexpr int kWinTile = D == 128 ? 128 : 64;
+// Warps: TMA, UMMA, TMEM owner, row terms (dK/dV only); then one elementwise
+// warp per 32 rows and 32 columns of a tile: 16 at d_k = 128, four per
+// scheduler (8 warps of 64 columns took twice what the tensor cores need: two
+// warps per scheduler do not cover their own latencies).
+template <int D>
+constexpr int kWinElemWarps = 4 * kWinTile<D> / 32;
+template <int D>
+constexpr int kWinBwdThreads = 128 + 32 * kWinElemWarps<D>;
+template <int D>
+constexpr int kWinBwdBlocks = D == 128 ? 1 : 2;  // per SM
 // Of every kWinBwdPolyEvery columns, kWinBwdPolyPairs pairs take their exp2
 // from a cubic on the FMA pipe (tiles without a mask).
 constexpr int kWinBwdPolyEvery = 16, kWinBwdPolyPairs = 3;
@@ -75,7 +86,7 @@ struct WindowBwdParams {
 // Query tiles that see the 128 keys from kb, of queries before row `limit`.
 struct WindowQueries {
   int start, end;  // rows; tiles end at `end`
-  __host__ __device__ int tiles() const { return end > start ? (end - start + 127) / 128 : 0; }
+  __host__ __device__ int tiles(int qt) const { return end > start ? (end - start + qt - 1) / qt : 0; }
 };
 __host__ __device__ inline WindowQueries window_queries(int nq, int nkv, int window, int sinks,
                                                         int kb, int limit) {
@@ -88,8 +99,8 @@ __host__ __device__ inline WindowQueries window_queries(int nq, int nkv, int win
   return q;
 }
 __host__ __device__ inline int window_parts(int nq, int nkv, int window, int sinks, int g, int kb,
-                                            int part_len) {
-  const int n = g * window_queries(nq, nkv, window, sinks, kb, nq).tiles();
+                                            int qt, int part_len) {
+  const int n = g * window_queries(nq, nkv, window, sinks, kb, nq).tiles(qt);
   return n <= part_len ? 1 : (n + part_len - 1) / part_len;
 }
 
@@ -222,8 +233,10 @@ __device__ __forceinline__ void win_ds32(const uint32_t (&dr)[32], const uint32_
 
 template <int D>
 struct WindowBwdCfg {
-  static constexpr int TILE = 128 * D * 2;
-  static constexpr int CHUNK = 128 * 128;
+  static constexpr int QT = kWinTile<D>;
+  static constexpr int TILE = 128 * D * 2;   // what stays: 128 rows
+  static constexpr int STREAM = QT * D * 2;  // what streams through
+  static constexpr int CHUNK = 128 * 128;    // 64 columns of 128 rows (d_k = 128 has two)
   // dK/dV: K, V, rings of Q (held from S_t to dK_t: three, so that the next
   // load never waits for a product in flight), dO (dP_t to dV_t) and row terms.
   // The barriers and shared words live behind them: with d_k = 128 the block
@@ -231,20 +244,23 @@ struct WindowBwdCfg {
   // part starts on the 1024-byte boundary that the swizzle needs.
   static constexpr int Q_SLOTS = D == 128 ? 3 : 4, DO_SLOTS = D == 128 ? 2 : 3, TERM_SLOTS = 2;
   static constexpr int KV_OFF_Q = 2 * TILE;
-  static constexpr int KV_OFF_DO = KV_OFF_Q + Q_SLOTS * TILE;
-  static constexpr int KV_OFF_TERMS = KV_OFF_DO + DO_SLOTS * TILE;
-  static constexpr int KV_OFF_BAR = KV_OFF_TERMS + TERM_SLOTS * 2 * 128 * 4;
+  static constexpr int KV_OFF_DO = KV_OFF_Q + Q_SLOTS * STREAM;
+  static constexpr int KV_OFF_TERMS = KV_OFF_DO + DO_SLOTS * STREAM;
+  static constexpr int KV_OFF_BAR = KV_OFF_TERMS + TERM_SLOTS * 2 * QT * 4;
   static constexpr int KV_SMEM = KV_OFF_BAR + 512;
   // dQ: Q, dO, rings of K (held until dQ_j) and V (until dP_j)
   static constexpr int QK_SLOTS = 3, QV_SLOTS = 2;
   static constexpr int Q_OFF_K = 2 * TILE;
-  static constexpr int Q_OFF_V = Q_OFF_K + QK_SLOTS * TILE;
-  static constexpr int Q_OFF_BAR = Q_OFF_V + QV_SLOTS * TILE;
+  static constexpr int Q_OFF_V = Q_OFF_K + QK_SLOTS * STREAM;
+  static constexpr int Q_OFF_BAR = Q_OFF_V + QV_SLOTS * STREAM;
   static constexpr int Q_SMEM = Q_OFF_BAR + 256 + 1024;
-  static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D;
+  static constexpr uint32_t COLS = D == 128 ? 512 : 256;  // tensor memory of a block
+  static constexpr uint32_t TM_S = 0, TM_DP = QT, TM_DV = 2 * QT, TM_DK = 2 * QT + D;
   // dQ: one score buffer (free once its tile is in registers), two of dP / dS
-  static constexpr uint32_t TQ_S = 0, TQ_DP = 128, TQ_A = 384;
-  static_assert(KV_SMEM <= 232448 && Q_SMEM <= 232448, "shared memory");
+  static constexpr uint32_t TQ_S = 0, TQ_DP = QT, TQ_A = 3 * QT;
+  static_assert(TM_DK + D <= COLS && TQ_A + D <= COLS, "tensor memory");
+  static_assert(kWinBwdBlocks<D> * (KV_SMEM + 1024) <= 233472 &&
+                    kWinBwdBlocks<D> * (Q_SMEM + 1024) <= 233472, "shared memory");
 };
 
 // A 128-row product with A from tensor memory, 64 columns of A: the packed
@@ -272,7 +288,7 @@ __device__ __forceinline__ uint4 win_pack8(const uint32_t* v, float f) {
 // ------------------------------------------------------------------ dK, dV --
 // Grid (parts of one (sequence, kv head), B * hkv).
 template <typename T, int D>
-__global__ void __launch_bounds__(kWinBwdThreads, 1)
+__global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     window_dkv_tc_kernel(const __grid_constant__ CUtensorMap mapQ,
                          const __grid_constant__ CUtensorMap mapK,
                          const __grid_constant__ CUtensorMap mapV,
@@ -317,7 +333,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     for (int b0 = 0; b0 < p.nblk; b0 += 32) {
       const int blk = b0 + lane;
       const int n = blk < p.nblk ? window_parts(p.nq, p.nkv, p.window, p.sinks, p.g, blk * 128,
-                                                p.part_len)
+                                                C::QT, p.part_len)
                                  : 0;
       int inc = n, sinc = n > 1 ? n : 0;
 #pragma unroll
@@ -351,13 +367,13 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < C::QT / 64; ++c) {
       mbar_init(p_half0 + 8 * c, 8);
       mbar_init(ds_half0 + 8 * c, 8);
     }
     for (int c = 0; c < C::TERM_SLOTS; ++c) {
       mbar_init(terms_full0 + 8 * c, 1);
-      mbar_init(terms_empty0 + 8 * c, 16);
+      mbar_init(terms_empty0 + 8 * c, kWinElemWarps<D>);
     }
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
@@ -365,7 +381,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(tmem_base_p), 512);
+    tmem_alloc(smem_u32(tmem_base_p), C::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -376,13 +392,13 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   const int jb = plan_sh[0], part = plan_sh[1], slot0 = plan_sh[2];
   const int kb = jb * 128;
   const WindowQueries wq = window_queries(p.nq, p.nkv, p.window, p.sinks, kb, len - off);
-  const int tiles = wq.tiles();
+  const int tiles = wq.tiles(C::QT);
   const int it0 = slot0 < 0 ? 0 : part * p.part_len;
   const int it1 = slot0 < 0 ? p.g * tiles : min(p.g * tiles, it0 + p.part_len);
   const int n_it = max(0, it1 - it0);
-  // (head of the group, query tile) of item it0; tile t starts at row t0 + 128 t
+  // (head of the group, query tile) of item it0; tile t starts at row t0 + QT t
   const int hl0 = tiles > 0 ? it0 / tiles : 0, tl0 = it0 - hl0 * tiles;
-  const int t0 = wq.end - 128 * tiles;
+  const int t0 = wq.end - C::QT * tiles;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -405,18 +421,18 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
           break;
         q_armed[qs] = static_cast<int>(qph);
         if (leader) {
-          mbar_arrive_expect_tx(q_full0 + 8 * qs, C::TILE);
-          tma_load_5d(smem_u32(smem + C::KV_OFF_Q + qs * C::TILE), &mapQ, q_full0 + 8 * qs, 0,
-                      t0 + 128 * tl, 0, kvh * p.g + hl, bidx);
+          mbar_arrive_expect_tx(q_full0 + 8 * qs, C::STREAM);
+          tma_load_5d(smem_u32(smem + C::KV_OFF_Q + qs * C::STREAM), &mapQ, q_full0 + 8 * qs, 0,
+                      t0 + C::QT * tl, 0, kvh * p.g + hl, bidx);
         }
         __syncwarp();
         if (!mbar_wait_warp(do_empty0 + 8 * ds, dph ^ 1u, abort_flag, p.err, kSiteAttnProducer))
           break;
         do_armed[ds] = static_cast<int>(dph);
         if (leader) {
-          mbar_arrive_expect_tx(do_full0 + 8 * ds, C::TILE);
-          tma_load_5d(smem_u32(smem + C::KV_OFF_DO + ds * C::TILE), &mapDO, do_full0 + 8 * ds, 0,
-                      t0 + 128 * tl, 0, kvh * p.g + hl, bidx);
+          mbar_arrive_expect_tx(do_full0 + 8 * ds, C::STREAM);
+          tma_load_5d(smem_u32(smem + C::KV_OFF_DO + ds * C::STREAM), &mapDO, do_full0 + 8 * ds, 0,
+                      t0 + C::QT * tl, 0, kvh * p.g + hl, bidx);
         }
         __syncwarp();
         if (++tl == tiles) {
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- UMMA issue
     const bool leader = elect_one();
-    constexpr uint32_t idesc_s = idesc16<T>(128, 128, false, false);
+    constexpr uint32_t idesc_s = idesc16<T>(128, C::QT, false, false);
     constexpr uint32_t idesc_o = idesc16<T>(128, D, false, true);
     const uint32_t k_lo = sdesc_lo(smem_u32(smem), 16);
     const uint32_t v_lo = sdesc_lo(smem_u32(smem + C::TILE), 16);
@@ -443,9 +459,9 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       if (leader) umma_commit(bar);
       __syncwarp();
     };
-    auto q_slot = [&](int t) { return smem_u32(smem + C::KV_OFF_Q + (t % C::Q_SLOTS) * C::TILE); };
+    auto q_slot = [&](int t) { return smem_u32(smem + C::KV_OFF_Q + (t % C::Q_SLOTS) * C::STREAM); };
     auto do_slot = [&](int t) {
-      return smem_u32(smem + C::KV_OFF_DO + (t % C::DO_SLOTS) * C::TILE);
+      return smem_u32(smem + C::KV_OFF_DO + (t % C::DO_SLOTS) * C::STREAM);
     };
     auto issue_s = [&](int t) -> bool {
       if (!mbar_wait_warp(q_full0 + 8 * (t % C::Q_SLOTS),
@@ -470,7 +486,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       return true;
     };
     auto issue_grad = [&](int t, uint32_t bar0, uint32_t acc, uint32_t a_tm, uint32_t b_lo) {
-      for (int hh = 0; hh < 2; ++hh) {
+      for (int hh = 0; hh < C::QT / 64; ++hh) {
         if (!mbar_wait_warp(bar0 + 8 * hh, static_cast<uint32_t>(t & 1), abort_flag, p.err,
                             kSiteAttnMma))
           return false;
@@ -506,21 +522,21 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     int tl = tl0;
     for (int t = 0; t < n_it; ++t) {
       const int ts = t % C::TERM_SLOTS;
-      float2 v[4];
+      float2 v[C::QT / 32];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = t0 + 128 * tl + lane + 32 * k;
-        v[k] = i >= 0 ? __ldg(rows + i) : make_float2(-INFINITY, 0.f);
+      for (int q = 0; q < C::QT / 32; ++q) {
+        const int i = t0 + C::QT * tl + lane + 32 * q;
+        v[q] = i >= 0 ? __ldg(rows + i) : make_float2(-INFINITY, 0.f);
       }
       if (!mbar_wait_warp(terms_empty0 + 8 * ts,
                           static_cast<uint32_t>((t / C::TERM_SLOTS) & 1) ^ 1u, abort_flag, p.err,
                           kSiteAttnProducer))
         break;
-      float* st = reinterpret_cast<float*>(smem + C::KV_OFF_TERMS) + ts * 256;
+      float* st = reinterpret_cast<float*>(smem + C::KV_OFF_TERMS) + ts * 2 * C::QT;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        st[lane + 32 * k] = v[k].x;
-        st[128 + lane + 32 * k] = v[k].y * sig;
+      for (int q = 0; q < C::QT / 32; ++q) {
+        st[lane + 32 * q] = v[q].x;
+        st[C::QT + lane + 32 * q] = v[q].y * sig;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(terms_full0 + 8 * ts);
@@ -541,8 +557,8 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     bool ok = n_it > 0;
     for (int t = 0; t < n_it && ok; ++t) {
       const int ts = t % C::TERM_SLOTS;
-      const float* st = reinterpret_cast<const float*>(smem + C::KV_OFF_TERMS) + ts * 256;
-      const int pq = off + t0 + 128 * tl;  // position of the tile's first query
+      const float* st = reinterpret_cast<const float*>(smem + C::KV_OFF_TERMS) + ts * 2 * C::QT;
+      const int pq = off + t0 + C::QT * tl;  // position of the tile's first query
       if (++tl == tiles) tl = 0;
       const uint32_t ph = static_cast<uint32_t>(t & 1);
       if (!mbar_wait_warp(terms_full0 + 8 * ts, static_cast<uint32_t>((t / C::TERM_SLOTS) & 1),
@@ -553,8 +569,8 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       }
       tc_fence_after();
       // every key of the block is seen by every query of the tile
-      const bool full = pq >= kb + 127 && (pq + 127 < kb + p.window || kb + 128 <= p.sinks);
-      const int q_lo = key - pq, q_hi = key < p.sinks ? 128 : key + p.window - pq;
+      const bool full = pq >= kb + 127 && (pq + C::QT - 1 < kb + p.window || kb + 128 <= p.sinks);
+      const int q_lo = key - pq, q_hi = key < p.sinks ? C::QT : key + p.window - pq;
       const uint32_t vis = full ? 0xFFFFFFFFu : bits_range(q_lo, q_hi, cc);
       uint32_t pr[32], pk[16];
       tmem_ld_32x32b_x32(t_lane + C::TM_S + cc * 32, pr);
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       uint32_t dr[32];
       tmem_ld_32x32b_x32(t_lane + C::TM_DP + cc * 32, dr);
       tmem_ld_wait();
-      auto nd = [&](int k) { return *reinterpret_cast<const float2*>(st + 128 + cc * 32 + k); };
+      auto nd = [&](int k) { return *reinterpret_cast<const float2*>(st + C::QT + cc * 32 + k); };
       if (full)
         win_ds32<T, true>(dr, pr, pk, sig, nd, vis);
       else
@@ -593,8 +609,8 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     }
     const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
     tc_fence_after();
-    // even column groups store dV, odd ones dK, each half of the columns
-    const int half = cc & 1, c0 = (cc >> 1) * (D / 64), c1 = c0 + D / 64;
+    // even column groups store dV, odd ones dK, sharing the d_k / 32 pieces
+    const int half = cc & 1;
     const float f = half == 0 ? exp2f(-WinScale<T>::kP) : p.scale / (sigma * WinScale<T>::kDS);
     const uint32_t acc = t_lane + (half == 0 ? C::TM_DV : C::TM_DK);
     if (slot0 >= 0) {
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
         float* dst = p.part + ((static_cast<long long>(bk) * p.split_parts + slot0 + part) * 2 + half) *
                                   (128 * D) + kr * D;
 #pragma unroll 1
-        for (int x = c0; x < c1; ++x) {
+        for (int x = cc >> 1; x < D / 32; x += C::QT / 64) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(acc + x * 32, v);
           tmem_ld_wait();
@@ -618,7 +634,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
                    ? static_cast<T*>(p.dv) + bidx * p.dv_b + key * p.dv_n + kvh * p.dv_h
                    : static_cast<T*>(p.dk) + bidx * p.dk_b + key * p.dk_n + kvh * p.dk_h;
 #pragma unroll 1
-      for (int x = c0; x < c1; ++x) {
+      for (int x = cc >> 1; x < D / 32; x += C::QT / 64) {
         uint32_t v[32];
         if (done) {
           tmem_ld_32x32b_x32(acc + x * 32, v);
@@ -636,7 +652,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, 512);
+  if (warp == 2) tmem_dealloc(tmem, C::COLS);
 }
 
 // Grid (cut blocks, B * hkv, 8): 32 rows of dV or dK of one block each, the
@@ -650,14 +666,14 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WindowBwdParams 
   // the blockIdx.x-th cut block and its first slot
   int blk = 0, slot = 0, seen = 0;
   for (;; ++blk) {
-    const int n = window_parts(p.nq, p.nkv, p.window, p.sinks, p.g, blk * 128, p.part_len);
+    const int n = window_parts(p.nq, p.nkv, p.window, p.sinks, p.g, blk * 128, kWinTile<D>, p.part_len);
     if (n <= 1) continue;
     if (seen == static_cast<int>(blockIdx.x)) break;
     ++seen;
     slot += n;
   }
   const int items = p.g * window_queries(p.nq, p.nkv, p.window, p.sinks, blk * 128,
-                                         len - (p.nkv - p.nq)).tiles();
+                                         len - (p.nkv - p.nq)).tiles(kWinTile<D>);
   const int parts = (items + p.part_len - 1) / p.part_len;  // those that have items
   const float* src = p.part + (static_cast<long long>(bk) * p.split_parts + slot) * (2 * 128 * D) +
                      which * (128 * D);
@@ -684,7 +700,7 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WindowBwdParams 
 // ---------------------------------------------------------------------- dQ --
 // Grid (query blocks, heads, B); the blocks with most keys first.
 template <typename T, int D>
-__global__ void __launch_bounds__(kWinBwdThreads, 1)
+__global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     window_dq_tc_kernel(const __grid_constant__ CUtensorMap mapQ,
                         const __grid_constant__ CUtensorMap mapK,
                         const __grid_constant__ CUtensorMap mapV,
@@ -715,7 +731,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   const int p0 = off + qb * 128;
   const int hi = min(off + min(p.nq, qb * 128 + 128), len);
   const bool any = hi > p0;
-  const WindowKeys kt = window_keys(max(0, p0 - p.window + 1), hi, p.sinks, any);
+  const WindowKeys<C::QT> kt = window_keys<C::QT>(max(0, p0 - p.window + 1), hi, p.sinks, any);
   const int n_kv = kt.n_s + kt.n_w;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -728,16 +744,16 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       mbar_init(v_empty0 + 8 * s, 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, 16);
+    mbar_init(s_free, kWinElemWarps<D>);
     for (int b = 0; b < 2; ++b) mbar_init(dp_full0 + 8 * b, 1);
-    for (int b = 0; b < 4; ++b) mbar_init(ds_half0 + 8 * b, 8);
+    for (int b = 0; b < 4; ++b) mbar_init(ds_half0 + 8 * b, 8);  // 8 warps per 64 columns
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     abort_sh = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(&tmem_base_sh), 512);
+    tmem_alloc(smem_u32(&tmem_base_sh), C::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -767,8 +783,8 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
           break;
         k_armed[ks] = static_cast<int>(kph);
         if (leader) {
-          mbar_arrive_expect_tx(k_full0 + 8 * ks, C::TILE);
-          tma_load_5d(smem_u32(smem + C::Q_OFF_K + ks * C::TILE), &mapK, k_full0 + 8 * ks, 0, key, 0,
+          mbar_arrive_expect_tx(k_full0 + 8 * ks, C::STREAM);
+          tma_load_5d(smem_u32(smem + C::Q_OFF_K + ks * C::STREAM), &mapK, k_full0 + 8 * ks, 0, key, 0,
                       kvh, bidx);
         }
         __syncwarp();
@@ -776,8 +792,8 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
           break;
         v_armed[vs] = static_cast<int>(vph);
         if (leader) {
-          mbar_arrive_expect_tx(v_full0 + 8 * vs, C::TILE);
-          tma_load_5d(smem_u32(smem + C::Q_OFF_V + vs * C::TILE), &mapV, v_full0 + 8 * vs, 0, key, 0,
+          mbar_arrive_expect_tx(v_full0 + 8 * vs, C::STREAM);
+          tma_load_5d(smem_u32(smem + C::Q_OFF_V + vs * C::STREAM), &mapV, v_full0 + 8 * vs, 0, key, 0,
                       kvh, bidx);
         }
         __syncwarp();
@@ -793,7 +809,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- UMMA issue
     const bool leader = elect_one();
-    constexpr uint32_t idesc_s = idesc16<T>(128, 128, false, false);
+    constexpr uint32_t idesc_s = idesc16<T>(128, C::QT, false, false);
     constexpr uint32_t idesc_o = idesc16<T>(128, D, false, true);
     const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
     const uint32_t do_lo = sdesc_lo(smem_u32(smem + C::TILE), 16);
@@ -801,8 +817,8 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       if (leader) umma_commit(bar);
       __syncwarp();
     };
-    auto k_slot = [&](int j) { return smem_u32(smem + C::Q_OFF_K + (j % C::QK_SLOTS) * C::TILE); };
-    auto v_slot = [&](int j) { return smem_u32(smem + C::Q_OFF_V + (j % C::QV_SLOTS) * C::TILE); };
+    auto k_slot = [&](int j) { return smem_u32(smem + C::Q_OFF_K + (j % C::QK_SLOTS) * C::STREAM); };
+    auto v_slot = [&](int j) { return smem_u32(smem + C::Q_OFF_V + (j % C::QV_SLOTS) * C::STREAM); };
     auto issue_s = [&](int j) -> bool {
       if (!mbar_wait_warp(k_full0 + 8 * (j % C::QK_SLOTS),
                           static_cast<uint32_t>((j / C::QK_SLOTS) & 1), abort_flag, p.err,
@@ -821,7 +837,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
         return false;
       tc_fence_after();
       if (leader)
-        bwd_issue_ss<D>(tmem + C::TQ_DP + 128u * static_cast<uint32_t>(j & 1), do_lo,
+        bwd_issue_ss<D>(tmem + C::TQ_DP + C::QT * static_cast<uint32_t>(j & 1), do_lo,
                         sdesc_lo(v_slot(j), 16), idesc_s);
       __syncwarp();
       commit(dp_full0 + 8 * (j & 1));
@@ -840,7 +856,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
         ok = ok && issue_s(j + 1) && issue_dp(j + 1);
         if (!ok) break;
       }
-      for (int hh = 0; hh < 2; ++hh) {
+      for (int hh = 0; hh < C::QT / 64; ++hh) {
         if (!mbar_wait_warp(ds_half0 + 16 * (j & 1) + 8 * hh, static_cast<uint32_t>((j >> 1) & 1),
                             abort_flag, p.err, kSiteAttnMma)) {
           ok = false;
@@ -849,7 +865,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
         tc_fence_after();
         if (leader)
           win_issue_ts_half<D>(tmem + C::TQ_A,
-                               tmem + C::TQ_DP + 128u * static_cast<uint32_t>(j & 1),
+                               tmem + C::TQ_DP + C::QT * static_cast<uint32_t>(j & 1),
                                sdesc_lo(k_slot(j), C::CHUNK), idesc_o, hh, j == 0);
         __syncwarp();
       }
@@ -884,7 +900,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
       tmem_ld_32x32b_x32(t_lane + C::TQ_S + cc * 32, pr);
       const int kb = kt.key(j);
       const bool sink = j < kt.n_s;
-      const bool full = !sink && kb + 127 <= p0 && kb >= kt.lo && kb >= p0 + 128 - p.window;
+      const bool full = !sink && kb + C::QT - 1 <= p0 && kb >= kt.lo && kb >= p0 + 128 - p.window;
       const uint32_t vis = full ? 0xFFFFFFFFu
                            : sink ? bits_range(0, kt.ns - kb, cc)
                                   : window_bits(pos, kb, kt.lo, p.window, p.sinks, cc);
@@ -902,7 +918,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t tP = t_lane + C::TQ_DP + 128u * static_cast<uint32_t>(j & 1) + cc * 32;
+      const uint32_t tP = t_lane + C::TQ_DP + C::QT * static_cast<uint32_t>(j & 1) + cc * 32;
       uint32_t dr[32];
       tmem_ld_32x32b_x32(tP, dr);
       tmem_ld_wait();
@@ -921,7 +937,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
     const float f = p.scale / (sigma * WinScale<T>::kDS);
     T* dst = static_cast<T*>(p.dq) + bidx * p.dq_b + i * p.dq_n + head * p.dq_h;
     // the column groups share the d_k / 32 pieces of the row
-    for (int x = cc; x < D / 32; x += 4) {
+    for (int x = cc; x < D / 32; x += C::QT / 32) {
       uint32_t v[32];
       if (done) {
         tmem_ld_32x32b_x32(t_lane + C::TQ_A + x * 32, v);
@@ -938,7 +954,7 @@ __global__ void __launch_bounds__(kWinBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, 512);
+  if (warp == 2) tmem_dealloc(tmem, C::COLS);
 }
 
 }  // namespace bpt

@@ -244,17 +244,17 @@ bpt_status ops_encoder() {
 }
 
 // Strided rows [batch, n, heads, d_k] viewed as [batch][heads][d_k/64][n][64]:
-// a box is 128 rows of one head, 64-column chunks one after another in shared
+// a box is `rows` rows of one head, 64-column chunks one after another in shared
 // memory (128-byte swizzle).  Rows outside 0 .. n-1 read as zeros.
 bool map_rows(CUtensorMap* m, const bpt_rows& r, int64_t batch, int64_t n, int64_t heads,
-              int64_t dk) {
+              int64_t dk, int rows = 128) {
   const int64_t any = 128;  // the stride of a dimension of one entry is not used
   cuuint64_t dims[5] = {64, cuuint64_t(n), cuuint64_t(dk / 64), cuuint64_t(heads),
                         cuuint64_t(batch)};
   cuuint64_t st[4] = {cuuint64_t(n > 1 ? r.stride_n * 2 : any), 128,
                       cuuint64_t(heads > 1 ? r.stride_h * 2 : any),
                       cuuint64_t(batch > 1 ? r.stride_b * 2 : any)};
-  cuuint32_t box[5] = {64, 128, cuuint32_t(dk / 64), 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  cuuint32_t box[5] = {64, cuuint32_t(rows), cuuint32_t(dk / 64), 1, 1}, es[5] = {1, 1, 1, 1, 1};
   return g_ops_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, r.data, dims, st, box, es,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -328,16 +328,18 @@ WindowBwdPlan window_bwd_plan(const bpt_window* w) {
   const int nq = int(w->n_q), nkv = int(w->n_kv), g = int(w->heads / w->kv_heads);
   const int win = int(std::min<int64_t>(w->window, nkv)), snk = int(std::min<int64_t>(w->sinks, nkv));
   const int nblk = (nkv + 127) / 128;
+  const int qt = w->d_k == 128 ? bpt::kWinTile<128> : bpt::kWinTile<64>;
+  const int blocks = w->d_k == 128 ? bpt::kWinBwdBlocks<128> : bpt::kWinBwdBlocks<64>;
   int64_t items = 0;
   for (int b = 0; b < nblk; ++b)
-    items += int64_t(g) * bpt::window_queries(nq, nkv, win, snk, b * 128, nq).tiles();
+    items += int64_t(g) * bpt::window_queries(nq, nkv, win, snk, b * 128, nq).tiles(qt);
   items *= w->batch * w->kv_heads;
-  // half of one SM's share, at least 8 items (a part costs 128 KB of traffic
+  // half of one resident block's share, at least 8 items (a part costs 128 KB of traffic
   // and a join, about what an item costs)
   p.part_len = int(std::min<int64_t>(0x7FFFFFFF, std::max<int64_t>(
-      8, (items + 2 * kPlanSms - 1) / (2 * kPlanSms))));
+      8, (items + 2 * blocks * kPlanSms - 1) / (2 * blocks * kPlanSms))));
   for (int b = 0; b < nblk; ++b) {
-    const int n = bpt::window_parts(nq, nkv, win, snk, g, b * 128, p.part_len);
+    const int n = bpt::window_parts(nq, nkv, win, snk, g, b * 128, qt, p.part_len);
     p.parts += n;
     if (n > 1) {
       p.cut_parts += n;
@@ -361,8 +363,8 @@ bpt_status check_window_bwd(const bpt_window* w) {
 }
 
 template <typename T, int D>
-cudaError_t launch_window_bwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                              const CUtensorMap& d_o, const bpt::WindowTermsParams& tp,
+cudaError_t launch_window_bwd(const CUtensorMap* stay, const CUtensorMap* stream,
+                              const bpt::WindowTermsParams& tp,
                               const bpt::WindowBwdParams& p, const WindowBwdPlan& plan,
                               int64_t batch, cudaStream_t s) {
   using C = bpt::WindowBwdCfg<D>;
@@ -370,14 +372,14 @@ cudaError_t launch_window_bwd(const CUtensorMap& q, const CUtensorMap& k, const 
   if (rows > 0)
     bpt::window_terms_kernel<T, D><<<unsigned((rows + per - 1) / per), 256, 0, s>>>(tp);
   bpt::window_dkv_tc_kernel<T, D>
-      <<<dim3(unsigned(plan.parts), unsigned(batch * p.hkv)), bpt::kWinBwdThreads, C::KV_SMEM, s>>>(
-          q, k, v, d_o, p);
+      <<<dim3(unsigned(plan.parts), unsigned(batch * p.hkv)), bpt::kWinBwdThreads<D>, C::KV_SMEM,
+         s>>>(stream[0], stay[1], stay[2], stream[3], p);
   if (plan.cut_blocks > 0)
     bpt::window_join_kernel<T, D>
         <<<dim3(unsigned(plan.cut_blocks), unsigned(batch * p.hkv), 8), 256, 0, s>>>(p);
   bpt::window_dq_tc_kernel<T, D>
-      <<<dim3(unsigned(p.nqb), unsigned(p.h), unsigned(batch)), bpt::kWinBwdThreads, C::Q_SMEM,
-         s>>>(q, k, v, d_o, p);
+      <<<dim3(unsigned(p.nqb), unsigned(p.h), unsigned(batch)), bpt::kWinBwdThreads<D>, C::Q_SMEM,
+         s>>>(stay[0], stream[1], stream[2], stay[3], p);
   return cudaGetLastError();
 }
 
@@ -647,10 +649,19 @@ bpt_status window_backward(const bpt_window* w, const bpt_rows* q, const bpt_row
   if (st != BPT_OK) return st;
   st = ops_encoder();
   if (st != BPT_OK) return st;
-  CUtensorMap mq, mk, mv, md;
-  if (!map_rows(&mq, *q, B, nq, h, c) || !map_rows(&mk, *k, B, nkv, hkv, c) ||
-      !map_rows(&mv, *v, B, nkv, hkv, c) || !map_rows(&md, *d_o, B, nq, h, c))
-    return BPT_ERR_CUDA;
+  // q, k, v, dO in boxes of 128 rows and of those that stream through a block
+  CUtensorMap stay[4], stream_maps[4];
+  const int qt = c == 128 ? bpt::kWinTile<128> : bpt::kWinTile<64>;
+  const bpt_rows* in[4] = {q, k, v, d_o};
+  for (int i = 0; i < 4; ++i) {
+    const bool is_q = i == 0 || i == 3;
+    const int64_t n = is_q ? nq : nkv, hh = is_q ? h : hkv;
+    if (!map_rows(&stay[i], *in[i], B, n, hh, c)) return BPT_ERR_CUDA;
+    if (qt == 128)
+      stream_maps[i] = stay[i];
+    else if (!map_rows(&stream_maps[i], *in[i], B, n, hh, c, qt))
+      return BPT_ERR_CUDA;
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* amax = nullptr;
@@ -691,11 +702,11 @@ bpt_status window_backward(const bpt_window* w, const bpt_rows* q, const bpt_row
   cudaError_t e;
   using bf = __nv_bfloat16;
   if (w->dtype == BPT_BF16)
-    e = c == 128 ? launch_window_bwd<bf, 128>(mq, mk, mv, md, tp, p, plan, B, s)
-                 : launch_window_bwd<bf, 64>(mq, mk, mv, md, tp, p, plan, B, s);
+    e = c == 128 ? launch_window_bwd<bf, 128>(stay, stream_maps, tp, p, plan, B, s)
+                 : launch_window_bwd<bf, 64>(stay, stream_maps, tp, p, plan, B, s);
   else
-    e = c == 128 ? launch_window_bwd<__half, 128>(mq, mk, mv, md, tp, p, plan, B, s)
-                 : launch_window_bwd<__half, 64>(mq, mk, mv, md, tp, p, plan, B, s);
+    e = c == 128 ? launch_window_bwd<__half, 128>(stay, stream_maps, tp, p, plan, B, s)
+                 : launch_window_bwd<__half, 64>(stay, stream_maps, tp, p, plan, B, s);
   return e == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
 
