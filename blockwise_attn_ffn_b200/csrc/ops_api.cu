@@ -368,9 +368,9 @@ cudaError_t launch_window_bwd(const CUtensorMap* stay, const CUtensorMap* stream
                               const bpt::WindowBwdParams& p, const WindowBwdPlan& plan,
                               int64_t batch, cudaStream_t s) {
   using C = bpt::WindowBwdCfg<D>;
-  const int64_t rows = batch * p.nq * p.h, per = 256 / (D / 8);
-  if (rows > 0)
-    bpt::window_terms_kernel<T, D><<<unsigned((rows + per - 1) / per), 256, 0, s>>>(tp);
+  const int64_t rows = int64_t(p.nq) * p.h, per = 256 / (D / 8) * bpt::kTermRows;
+  bpt::window_terms_kernel<T, D>
+      <<<dim3(unsigned((rows + per - 1) / per), unsigned(batch)), 256, 0, s>>>(tp);
   bpt::window_dkv_tc_kernel<T, D>
       <<<dim3(unsigned(plan.parts), unsigned(batch * p.hkv)), bpt::kWinBwdThreads<D>, C::KV_SMEM,
          s>>>(stream[0], stay[1], stay[2], stream[3], p);
