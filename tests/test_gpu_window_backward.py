@@ -79,6 +79,8 @@ CASES = [
     (1, 2048, 2048, 1, 1, 128, 256, 4, "bf16", None, True),
     (1, 512, 512, 1, 1, 64, 255, 200, "bf16", None, False),
     (1, 3000, 3000, 4, 1, 64, 200, 4, "f16", [2999], False),      # sinks cut into parts
+    (13, 900, 900, 9, 3, 128, 150, 3, "bf16", list(range(0, 910, 70)), False),
+    (15, 1000, 1030, 7, 7, 128, 260, 200, "f16", None, False),
 ]
 
 
