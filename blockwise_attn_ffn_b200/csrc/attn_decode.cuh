@@ -94,6 +94,11 @@ __device__ __forceinline__ DecodeSeq decode_seq(const DecodeParams& p, uint32_t 
 __device__ __forceinline__ uint32_t run_start(uint32_t W, uint32_t G, uint32_t c) {
   return static_cast<uint32_t>(static_cast<unsigned long long>(W) * c / G);
 }
+// Runs of W tiles: none is empty.  (Longer runs for short caches measured slower: a
+// run pays 2 to 3 us for every pair that it ends, a part of a pair little more.)
+__device__ __forceinline__ uint32_t decode_runs(const DecodeParams& p, uint32_t W) {
+  return min(p.ctas, W);
+}
 // The run that covers tile x < W.
 __device__ __forceinline__ uint32_t run_of(uint32_t W, uint32_t G, uint32_t x) {
   uint32_t c = static_cast<uint32_t>((static_cast<unsigned long long>(x) * G) / W);
@@ -162,10 +167,13 @@ struct DecodeCfg {
   static constexpr int SUB = 16 * D * 2;       // 16 rows of K or of V
   static constexpr int STAGE = 2 * SUB;
   static constexpr int STAGES = DecodeShape<D, NT>::RING / (kDecodeWarps * STAGE);
-  static constexpr int RED_LD = D + 8;         // floats
+  static constexpr int RED_LD = D + 4;         // floats; four head pairs and 8 rows meet 32 banks
+  static constexpr int BUFS = NT == 1 ? 2 : 1;  // join buffers (16 heads: two blocks fill the SM)
   static constexpr int OFF_RED = kDecodeWarps * STAGES * STAGE;
-  static constexpr int OFF_ML = OFF_RED + ROWS * RED_LD * 4;
+  static constexpr int OFF_ML = OFF_RED + BUFS * ROWS * RED_LD * 4;
   static constexpr int SMEM = OFF_ML + kDecodeWarps * ROWS * 8;
+  // (with 1 KB of the SM's and up to 1 KB of static shared memory per block)
+  static_assert(DecodeShape<D, NT>::CTAS * (SMEM + 2048) <= 233472, "blocks per SM");
 };
 
 // Sum over the block of one value per thread.
@@ -230,26 +238,21 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
   __shared__ uint32_t vmask[kDecodeWarps][C::STAGES];
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t per = p.c.hkv * p.chunks;
-  const uint32_t W = decode_total(p, per, scratch);
-  // sequences without visible slots: zeros
-  for (uint32_t b = blockIdx.x; b < p.B; b += gridDim.x) {
-    bool bad = false;
-    const bool none = decode_seq(p, b, bad).n == 0;
-    if (bad && tid == 0) record_error(p.c.err, kErrIndex, kSiteDecode);
-    if (!none) continue;
-    for (uint32_t x = tid; x < p.h * (D / 8); x += kDecodeThreads)
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + b * p.o_b + (x / (D / 8)) * p.o_h +
-                                x % (D / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
+  // All tiles of the batch, W, cut into G runs (none empty), and the sequence of
+  // this run's first tile, w0: with up to 128 sequences in one pass over the
+  // lengths, else one for W and one that stops at w0.
+  uint32_t W = 0, G = 0, w0 = 0, w1 = 0, base = 0;
+  const bool one_pass = p.B <= kDecodeThreads;
+  if (!one_pass) {
+    W = decode_total(p, per, scratch);
+    G = decode_runs(p, W);
+    w0 = run_start(W, G, blockIdx.x);
   }
-  const uint32_t G = min(p.ctas, W);  // no run is empty
-  if (blockIdx.x >= G) return;        // the whole block
-  const uint32_t w0 = run_start(W, G, blockIdx.x), w1 = run_start(W, G, blockIdx.x + 1);
-  // the sequence of tile w0: blocks of sequences, scanned until it is found
-  uint32_t base = 0;
   for (uint32_t b0 = 0; b0 < p.B; b0 += kDecodeThreads) {
     bool bad = false;
     const uint32_t b = b0 + tid;
     const uint32_t mine = b < p.B ? decode_seq(p, b, bad).tiles() * per : 0;
+    if (bad && blockIdx.x == 0) record_error(p.c.err, kErrIndex, kSiteDecode);
     uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -257,20 +260,31 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
       if (lane >= static_cast<uint32_t>(o)) inc += x;
     }
     if (lane == 31) scratch[warp] = inc;
+    // sequences without visible slots: zeros, by block b % grid
+    if (b < p.B && mine == 0 && b % gridDim.x == blockIdx.x)
+      for (uint32_t x = 0; x < p.h * (D / 8); ++x)
+        *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + b * p.o_b + (x / (D / 8)) * p.o_h +
+                                  x % (D / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     uint32_t off = base, tot = 0;
     for (uint32_t w = 0; w < kDecodeWarps; ++w) {
       if (w < warp) off += scratch[w];
       tot += scratch[w];
     }
-    if (off + inc - mine <= w0 && w0 < off + inc) {
+    if (one_pass) {
+      W = tot;
+      G = decode_runs(p, W);
+      w0 = run_start(W, G, blockIdx.x);
+    }
+    if (blockIdx.x < G && off + inc - mine <= w0 && w0 < off + inc) {
       find_sh[0] = b;
       find_sh[1] = off + inc - mine;
     }
     __syncthreads();
     base += tot;
-    if (base > w0) break;
   }
+  if (blockIdx.x >= G) return;  // the whole block
+  w1 = run_start(W, G, blockIdx.x + 1);
 
   // A position in the tile list: sequence, pair in it, tile in the pair.
   struct Cursor {
@@ -510,9 +524,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
             M = fmaxf(M, ml[w * C::ROWS + 8 * nt + c0 + j].x);
           f[nt][j] = m[nt][j] == -INFINITY ? 0.f : ex2_approx(m[nt][j] - M);
         }
+      // the first BUFS warps store, the others add to their buffer in turn
 #pragma unroll 1
-      for (uint32_t w = 0; w < kDecodeWarps; ++w) {
-        if (warp == w) {
+      for (uint32_t round = 0; round < kDecodeWarps / C::BUFS; ++round) {
+        if (warp / C::BUFS == round) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -521,9 +536,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
               for (int x = 0; x < 4; ++x) {
                 const uint32_t row = 8 * nt + c0 + (x & 1);
                 if (row >= heads) continue;
-                float* d = red + row * C::RED_LD + 16 * i + r0 + 8 * (x >> 1);
+                float* d = red + (warp % C::BUFS * C::ROWS + row) * C::RED_LD + 16 * i + r0 + 8 * (x >> 1);
                 const float v = o[i][nt][x] * f[nt][x & 1];
-                *d = w == 0 ? v : *d + v;
+                *d = round == 0 ? v : *d + v;
               }
         }
         __syncthreads();
@@ -534,7 +549,12 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
       constexpr uint32_t kLanes = D / 4;  // threads of a row, four columns each
       const uint32_t col = tid % kLanes * 4;
       for (uint32_t row = tid / kLanes; row < heads; row += kDecodeThreads / kLanes) {
-        const float4 v = *reinterpret_cast<const float4*>(red + row * C::RED_LD + col);
+        float4 v = *reinterpret_cast<const float4*>(red + row * C::RED_LD + col);
+        if constexpr (C::BUFS == 2) {
+          const float4 y =
+              *reinterpret_cast<const float4*>(red + (C::ROWS + row) * C::RED_LD + col);
+          v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+        }
         float M = -INFINITY, L = 0.f;
         for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, ml[w * C::ROWS + row].x);
         for (int w = 0; w < kDecodeWarps; ++w) {

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
                          const __grid_constant__ CUtensorMap mapV,
                          const __grid_constant__ CUtensorMap mapDO, const WindowBwdParams p) {
   using C = WindowBwdCfg<D>;
-  extern __shared__ __align__(1024) uint8_t win_smem[];
+  extern __shared__ __align__(128) uint8_t win_smem[];
   uint8_t* smem = win_smem;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::KV_OFF_BAR);
   const uint32_t kv_full = smem_u32(bars + 0);
