@@ -22,7 +22,7 @@ import torch
 from . import _lib
 
 _DTYPES = {torch.bfloat16: _lib.BPT_BF16, torch.float16: _lib.BPT_F16}
-HEADER_BYTES = 256
+HEADER_BYTES = 4096  # BPT_OPS_HEADER_BYTES
 
 
 def code_of(t: torch.Tensor, what: str) -> int:
@@ -120,7 +120,7 @@ def attn_decode_workspace(q: torch.Tensor, k_cache: torch.Tensor, page_table: to
                                                      with_acc)
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_decode_workspace_size")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=k_cache.device)
+    return new_workspace(nbytes, k_cache.device)
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

@@ -24,7 +24,8 @@
 //    grows by more than 2^8.
 // A run that covers all tiles of its pair writes the output; otherwise its
 // unnormalised fp32 accumulator and (m, l) go to the workspace, and the run
-// that comes last (a counter per pair, left at zero again) joins the parts in
+// that comes last (a counter per run that starts
+// such a pair, left at zero again) joins the parts in
 // run order: one launch, and results do not depend on timing.  A second kernel
 // adds the weights up where they are wanted.  P is rounded to the cache's type for the PV product (relative
 // error half a step, averaged over the keys); scores, statistics and sums are
@@ -66,7 +67,7 @@ struct DecodeParams {
   float* part_o;   // [2 * ctas][16][D]
   float2* part_ml; // [2 * ctas][16]
   float2* seg_ml;  // [B * h_kv * chunks][16]: joined (m, l), where weights are wanted
-  uint32_t* count; // [B * h_kv * chunks]: parts of the pair that are done
+  uint32_t* count; // [ctas]: parts that are done of the pair that run c starts and does not end
   uint32_t ctas;   // grid of the split kernel
   float* scores;   // nullable [B][h][scores_ld]: s log2(e) of the visible slots, dense
   long long scores_ld;
@@ -578,8 +579,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
         if (tid == 0) {
           const uint32_t s0 = cc.base + cc.pair * cc.tiles;
           const uint32_t lo = run_of(W, G, s0), hi = run_of(W, G, s0 + cc.tiles - 1);
-          const bool last = atomicAdd(p.count + seg, 1u) == hi - lo;
-          if (last) p.count[seg] = 0;
+          const bool last = atomicAdd(p.count + lo, 1u) == hi - lo;
+          if (last) p.count[lo] = 0;
           join_sh[0] = last ? 1u : 0u;
           join_sh[1] = lo;
           join_sh[2] = hi;

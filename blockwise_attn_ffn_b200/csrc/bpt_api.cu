@@ -826,14 +826,15 @@ bpt_status forward_bf16(const Plan& P, const void* x, const void* ln1, const voi
           rv{qkv + 2 * d, P.N * 3 * d, 3 * d, P.dk}, ro{o_keep, P.N * d, d, P.dk};
       LaunchScope ls(BPT_KIND_ATTN, s);
       const bpt_status st =
-          bpt_host::window_forward(&w, &rq, &rk, &rv, form->lens, &ro, stats, ws, kHeaderBytes,
+          bpt_host::window_forward(&w, &rq, &rk, &rv, form->lens, &ro, stats, ws, bpt_host::kOpsHeader,
                                    reinterpret_cast<bpt_stream_t>(s), err);
       if (st != BPT_OK) return st;
     }
     if (form->cache != nullptr) {
       const bpt_status st = bpt_host::cache_append(
           form->cache, qkv + d, qkv + 2 * d, P.N, heads_stride, form->lens, form->new_lens,
-          form->acc, form->pos, form->seen, ws, kHeaderBytes, reinterpret_cast<bpt_stream_t>(s),
+          form->acc, form->pos, form->seen, ws, bpt_host::kOpsHeader,
+          reinterpret_cast<bpt_stream_t>(s),
           err);
       if (st != BPT_OK) return st;
     }
@@ -879,7 +880,7 @@ bpt_status forward_bf16(const Plan& P, const void* x, const void* ln1, const voi
       LaunchScope ls(BPT_KIND_ATTN, s);
       bpt_status st = bpt_host::cache_append(&c, qkv + d, qkv + 2 * d, 1, kv_stride, nullptr,
                                              form->new_lens, form->acc, form->pos, form->seen, ws,
-                                             kHeaderBytes, st_, err);
+                                             bpt_host::kOpsHeader, st_, err);
       if (st != BPT_OK) return st;
       c.lens = form->new_lens;
       st = bpt_host::attn_decode(&c, qkv, P.h, 3 * d, P.dk, form->window, form->sinks, form->acc,
@@ -1562,7 +1563,7 @@ bpt_status layer_forward_impl(const void* x, const void* ln1, const void* W_Q, c
                                                        P.off_qkv) + d;
     const int64_t st6[6] = {N * 3 * d, 3 * d, P.dk, N * 3 * d, 3 * d, P.dk};
     st = bpt_host::cache_append(&c, kv, kv + d, N, st6, form->lens, form->new_lens, form->acc,
-                                form->pos, form->seen, workspace, kHeaderBytes, stream, nullptr,
+                                form->pos, form->seen, workspace, bpt_host::kOpsHeader, stream, nullptr,
                                 true);
     if (st != BPT_OK) return st;
     const size_t rows = size_t(c.pages) * size_t(c.kv_heads * c.page_size) * size_t(c.d_k) * 2;
@@ -2201,7 +2202,7 @@ bpt_status bpt_layer_decode_prepare(const void* W_Q, const void* W_K, const void
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (cudaMemsetAsync(ws, 0, kHeaderBytes, s) != cudaSuccess ||
-      cudaMemsetAsync(ws + dp.off_attn, 0, dp.attn_bytes, s) != cudaSuccess)
+      cudaMemsetAsync(ws + dp.off_attn, 0, bpt_host::kOpsHeader, s) != cudaSuccess)
     return BPT_ERR_CUDA;
   bpt::CvtSegments cs{};
   __half* dst = reinterpret_cast<__half*>(ws + dp.P.off_w16);
@@ -2262,7 +2263,7 @@ bpt_status bpt_layer_decode(const void* x, const void* ln1, const void* ln2, con
     const __half* q = reinterpret_cast<const __half*>(w + dp.P.off_qkv);
     const int64_t dk = dp.P.dk, st6[6] = {3 * d, 3 * d, dk, 3 * d, 3 * d, dk};
     st = bpt_host::cache_append(cache, q + d, q + 2 * d, 1, st6, nullptr, new_lens, acc, pos, seen,
-                                w, kHeaderBytes, stream, nullptr, true);
+                                w, bpt_host::kOpsHeader, stream, nullptr, true);
     if (st != BPT_OK) return st;
     st = bpt_host::attn_decode(cache, q, dp.P.h, 3 * d, dk, window, sinks, acc, acc,
                                w + dp.P.off_o, d, dk, w + dp.off_attn, dp.attn_bytes, stream,

@@ -3,9 +3,10 @@
 // with a sliding window (forward, backward).  Argument checks, workspace
 // layouts and launches; nothing is allocated and nothing synchronises.
 //
-// Workspaces: the first kOpsHeader bytes hold the error word, zeroed by the
-// caller once (bpt_read_device_error clears it after reading a fault), so a
-// call launches nothing but its own kernels.
+// Workspaces: the first kOpsHeader bytes hold the error word and counters,
+// zeroed by the caller once (every call leaves the counters at zero,
+// bpt_read_device_error clears the error word), so a call launches nothing but
+// its own kernels.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -29,7 +30,8 @@
 
 namespace {
 
-constexpr size_t kOpsHeader = 256;
+using bpt_host::kOpsHeader;
+constexpr size_t kCountOffset = 256;  // decode: counters of split pairs, one per block
 static_assert(bpt::kErrIndex == BPT_ERR_INDEX, "status code");
 
 size_t align_to(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -182,7 +184,7 @@ CacheLayout cache_layout(const bpt_cache* c) {
 }
 
 struct DecodeLayout {
-  size_t off_count, off_o, off_ml, off_seg, off_scores, total;
+  size_t off_o, off_ml, off_seg, off_scores, total;
   int64_t chunks, rows;
 };
 // Row length of the saved scores (dense over the visible slots), even.
@@ -200,8 +202,9 @@ bpt_status decode_layout(const bpt_cache* c, int64_t heads, int with_acc, Decode
       c->batch * c->kv_heads >= (int64_t(1) << 31))
     return BPT_ERR_UNSUPPORTED;
   const size_t parts = size_t(2 * bpt::kDecodeMaxCtas * bpt::kDecodeMaxSms) * 16;
-  l->off_count = kOpsHeader;
-  l->off_o = align_to(l->off_count + size_t(pairs) * 4, 256);
+  static_assert(kCountOffset + bpt::kDecodeMaxCtas * bpt::kDecodeMaxSms * 4 <= kOpsHeader,
+                "counters");
+  l->off_o = kOpsHeader;
   l->off_ml = align_to(l->off_o + parts * size_t(c->d_k) * 4, 256);
   l->off_seg = align_to(l->off_ml + parts * 8, 256);
   l->off_scores = align_to(l->off_seg + size_t(pairs) * 16 * 8, 256);
@@ -408,8 +411,9 @@ bpt_status cache_append(const bpt_cache* cache, const void* k_new, const void* v
   if (tokens > 0) {
     for (const void* p : {k_new, v_new})
       if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
+    const int64_t dims[3] = {B, tokens, h};  // (a dimension of one entry has no stride)
     for (int i = 0; i < 6; ++i)
-      if (strides[i] < 0 || strides[i] % 8 != 0) return BPT_ERR_INVALID_ARG;
+      if (dims[i % 3] > 1 && (strides[i] < 0 || strides[i] % 8 != 0)) return BPT_ERR_INVALID_ARG;
     if (tokens >= (int64_t(1) << 31) / (h * dk / 8)) return BPT_ERR_UNSUPPORTED;
   }
   const Range rk(cache->k, cache_bytes(cache)), rv(cache->v, cache_bytes(cache)),
@@ -475,8 +479,10 @@ bpt_status attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
   const int64_t B = cache->batch, dk = cache->d_k;
   for (const void* p : {q, static_cast<const void*>(out)})
     if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
-  for (int64_t x : {q_stride_b, q_stride_h, out_stride_b, out_stride_h})
-    if (x < 0 || x % 8 != 0) return BPT_ERR_INVALID_ARG;
+  auto bad_stride = [](int64_t n, int64_t x) { return n > 1 && (x < 0 || x % 8 != 0); };
+  if (bad_stride(B, q_stride_b) || bad_stride(heads, q_stride_h) || bad_stride(B, out_stride_b) ||
+      bad_stride(heads, out_stride_h))
+    return BPT_ERR_INVALID_ARG;
   // output rows must not meet one another
   if ((heads > 1 && out_stride_h < dk) || (B > 1 && out_stride_b < dk) ||
       (B > 1 && heads > 1 && out_stride_b < (heads - 1) * out_stride_h + dk &&
@@ -517,7 +523,7 @@ bpt_status attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
   p.window = clamp_u31(window);
   p.sinks = clamp_u31(sinks);
   p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(dk)));
-  p.count = reinterpret_cast<uint32_t*>(ws + l.off_count);
+  p.count = reinterpret_cast<uint32_t*>(ws + kCountOffset);
   p.part_o = reinterpret_cast<float*>(ws + l.off_o);
   p.part_ml = reinterpret_cast<float2*>(ws + l.off_ml);
   p.seg_ml = reinterpret_cast<float2*>(ws + l.off_seg);

@@ -615,15 +615,17 @@ bpt_status bpt_layer_forward_static(const void* x, const void* ln1, const void* 
  * its rows are not written), and BPT_ERR_INDEX is recorded for
  * bpt_read_device_error.
  *
- * Workspaces of these operators: 256-byte aligned, the FIRST 256 BYTES ZEROED
- * BY THE CALLER ONCE before the first use (the error word lives there; it
- * keeps the first fault until bpt_read_device_error returns and clears it).
- * bpt_attn_decode's workspace is zeroed whole, once: it holds counters that
- * every call leaves at zero.  The rest needs no initialisation.  Calls that may
- * overlap on the GPU
+ * Workspaces of these operators: 256-byte aligned, the FIRST
+ * BPT_OPS_HEADER_BYTES ZEROED BY THE CALLER ONCE before the first use (the
+ * error word, which keeps the first fault until bpt_read_device_error returns
+ * and clears it, and counters that every call leaves at zero).  The rest needs
+ * no initialisation, and one workspace that is large enough may serve any of
+ * these operators and sizes in turn.  Calls that may overlap on the GPU
  * (different streams, graphs launched side by side) need a workspace each.
  * All calls may be captured into a CUDA graph.
  */
+#define BPT_OPS_HEADER_BYTES 4096u
+
 typedef struct {
   void* k;
   void* v;
@@ -635,7 +637,7 @@ typedef struct {
 } bpt_cache;
 
 /* Workspace bytes of bpt_cache_append and bpt_cache_evict (pointers of the
- * cache are not looked at).  Append alone needs only the 256-byte header. */
+ * cache are not looked at).  Append alone needs only the header. */
 bpt_status bpt_cache_workspace_size(const bpt_cache* cache, size_t* bytes);
 
 /*
@@ -719,8 +721,7 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
  * Only what a row sees counts: NaN and infinities in keys and values that it
  * does not see (masked ones, padding) do not reach its output.
  *
- * Workspaces: as for the cache's operators (first 256 bytes zeroed once by
- * the caller; one per call that may overlap with another).
+ * Workspaces: as for the cache's operators.
  */
 typedef struct {
   int64_t batch, n_q, n_kv, heads, kv_heads, d_k;

@@ -75,7 +75,7 @@ def test_bad_caches(fields, want):
     (dict(strides=(384, 128, 64, -8, 128, 64)), INV), (dict(new_lens=None), INV),
     (dict(new_lens=addr(3)), INV), (dict(acc=addr(0)), INV), (dict(pos=addr(4) + 1), INV),
     (dict(k=addr(0) + 4096), INV), (dict(ws=None), INV), (dict(ws=addr(7) + 16), INV),
-    (dict(nbytes=255), WS), (dict(tokens=1 << 30), UNS), (dict(counts=addr(6)), INV),
+    (dict(nbytes=4095), WS), (dict(tokens=1 << 30), UNS), (dict(counts=addr(6)), INV),
     (dict(seen=addr(6)), INV), (dict(acc=addr(8), pos=addr(8)), INV),
 ], ids=str)
 def test_bad_appends(kw, want):
@@ -113,7 +113,7 @@ def test_empty_batches_do_nothing():
 
 def test_workspace_sizes():
     st, a = bpt.bpt_cache_workspace_size(cache())
-    assert st == bpt.BPT_OK and a >= 256 + 4 * 4 * 2 * 128
+    assert st == bpt.BPT_OK and a >= 4096 + 4 * 4 * 2 * 128
     st, b = bpt.bpt_attn_decode_workspace_size(cache(), 8, 0)
     st2, c = bpt.bpt_attn_decode_workspace_size(cache(), 8, 1)
     assert st == st2 == bpt.BPT_OK and c - b >= 4 * 8 * 128 * 4

@@ -162,6 +162,31 @@ def test_decode_strides_streams_and_repeats():
     assert torch.equal(acc_b, acc_a)
 
 
+def test_one_workspace_serves_sizes_and_operators_in_turn():
+    """Calls of different batches, heads and lengths, an append and an eviction
+    through one workspace: each gives what it gives with its own."""
+    cases = [([2000], 8, 1, 128, True), ([700, 90, 3] * 20, 8, 8, 64, False),
+             ([5000, 1], 4, 4, 128, True), ([300] * 70, 2, 1, 64, False)]
+    made = []
+    for i, (lens, h, hkv, dk, with_acc) in enumerate(cases):
+        pool = Pool(40 + i, lens, hkv, dk, 16, torch.bfloat16)
+        q = randn(gen(50 + i), (len(lens), h, dk), torch.bfloat16)
+        acc = torch.zeros((len(lens), hkv, pool.cap), device="cuda") if with_acc else None
+        size = bpt.attn_decode_workspace(q, pool.k, pool.table, with_acc).numel()
+        size = max(size, bpt.cache_workspace(pool.k, pool.table).numel())
+        made.append((pool, q, acc, size))
+    ws = torch.randint(0, 255, (max(m[3] for m in made),), dtype=torch.uint8, device="cuda")
+    ws[:4096] = 0
+    for turn in range(2):
+        for pool, q, acc, _ in made:
+            run = lambda w: bpt.attn_decode(q, pool.k, pool.v, pool.table, pool.lens, acc=acc,
+                                            acc_out=None if acc is None else acc.clone(), ws=w)
+            assert torch.equal(run(ws), run(None))
+            a, p, seen = evict_inputs(pool, 60, False)
+            bpt.cache_evict(pool.k, pool.v, pool.table, pool.lens, a, p, seen, max(pool.n), ws=ws)
+    no_fault(ws)
+
+
 def test_decode_in_a_graph_follows_the_lengths():
     lens = [100, 400]
     pool = Pool(5, [500, 500], 2, 64, 16, torch.float16)
