@@ -23,6 +23,7 @@ from . import _lib
 
 _DTYPES = {torch.bfloat16: _lib.BPT_BF16, torch.float16: _lib.BPT_F16}
 HEADER_BYTES = 4096  # BPT_OPS_HEADER_BYTES
+_Strides = ctypes.c_int64 * 6
 
 
 def code_of(t: torch.Tensor, what: str) -> int:
@@ -143,7 +144,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     if new_lens is None:
         new_lens = torch.empty_like(lens)
     ws = new_workspace(HEADER_BYTES, k_cache.device) if ws is None else check_workspace(ws, index)
-    strides = (ctypes.c_int64 * 6)(*k.stride()[:3], *v.stride()[:3])
+    strides = _Strides(*k.stride()[:3], *v.stride()[:3])
     st = run(_lib.bpt_cache_append, index, c, kp, vp, T, strides,
              None if counts is None else check(counts, "counts", (B,), torch.int32, index),
              check(new_lens, "new_lens", (B,), torch.int32, index),

@@ -8,8 +8,9 @@
 // byte and query head nothing else comes near.  So the kernel is built around
 // a steady stream of loads:
 //  - The work is the flat list of 64-slot tiles of all (sequence, kv head)
-//    pairs, cut into equal runs, one per CTA (fewer runs if there are fewer tiles), whatever the lengths: a long
-//    sequence is split over many CTAs, short ones share one.  The lengths are
+//    pairs, cut into equal runs, one per CTA (fewer if there are fewer tiles),
+//    whatever the lengths: a long sequence is split over many CTAs, short ones
+//    share one.  The lengths are
 //    read on the device, so no plan has to be made for a batch.
 //  - The query heads that share a kv head are the 8 columns of one warp MMA
 //    (m16n8k16; two of them for more than 8 heads) whose 16 rows are slots:

@@ -29,6 +29,12 @@
 // operands' type for the product with V (half a step per weight, of both
 // signs); scores, statistics and O are fp32; l sums the unrounded weights.
 //
+// Measured at 65536 tokens, 16 heads of 128, window 4096, 4 sinks: 1.97 ms in
+// bursts (1082 TFLOP/s of visible pairs), 2.28 ms under the power cap.  With two
+// threads per row (maxima exchanged through shared memory) it took 2.18 to 2.35
+// ms: the exponentials of a tile keep the scheduler's unit busy as long, and the
+// exchange comes on top.
+//
 // A masked key has weight 0, but 0 x V_j is NaN if V_j holds NaN or infinity.
 // Rows whose result is not finite are therefore done again, key by key over
 // what they see (window_row_slow): exact, and free for finite values.
