@@ -13,8 +13,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .cache import (HEADER_BYTES, check, check_workspace, code_of, new_workspace, rows_check, run,
-                    stream_of)
+from .cache import (HEADER_BYTES, check, check_workspace, code_of, current_stream, new_workspace,
+                    on_stream, rows_check, run)
 
 
 def _window(q, k, window, sinks) -> "_lib.Window":
@@ -46,6 +46,9 @@ def attn_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, windo
     the keys j <= p with p - j < window or j < sinks, for rows p < lens[b]
     (others give 0); returns out [B, Nq, h, d_k].  stats: an fp32
     [B, h, Nq, 2] tensor that receives (m, l) per row, for the backward."""
+    if stream is not None:
+        with on_stream(stream, q):
+            return attn_window_forward(q, k, v, window, sinks, lens, out, stats, ws)
     w = _window(q, k, window, sinks)
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
@@ -60,7 +63,7 @@ def attn_window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, windo
     st = run(_lib.bpt_attn_window_forward, index, w, _rows(q, "q", qs, dt, index),
              _rows(k, "k", ks, dt, index), _rows(v, "v", ks, dt, index), lp,
              _rows(out, "out", qs, dt, index), sp, ws.data_ptr(), ws.numel(),
-             stream_of(stream, index))
+             current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_window_forward")
     return out
@@ -83,6 +86,9 @@ def attn_window_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
                          stream: Optional[torch.cuda.Stream] = None):
     """(dq, dk, dv) of ``attn_window_forward``: o and stats from it, d_o the
     gradient of o; written to grads if given (any positive strides)."""
+    if stream is not None:
+        with on_stream(stream, q):
+            return attn_window_backward(q, k, v, o, stats, d_o, window, sinks, lens, grads, ws)
     w = _window(q, k, window, sinks)
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
@@ -103,7 +109,7 @@ def attn_window_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
              check(stats, "stats", (B, h, nq, 2), torch.float32, index),
              _rows(d_o, "d_o", qs, dt, index), lp, _rows(grads[0], "dq", qs, dt, index),
              _rows(grads[1], "dk", ks, dt, index), _rows(grads[2], "dv", ks, dt, index),
-             ws.data_ptr(), ws.numel(), stream_of(stream, index))
+             ws.data_ptr(), ws.numel(), current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_window_backward")
     return grads

@@ -33,9 +33,17 @@ def code_of(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def stream_of(stream: Optional[torch.cuda.Stream], index: int) -> int:
-    """The raw stream of a call on device `index` (the current one's by default)."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+def current_stream(index: int) -> int:
+    """The raw current stream of device `index`."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def on_stream(stream: torch.cuda.Stream, t: torch.Tensor):
+    """Makes `stream` current for a call on t's device: what the call allocates
+    and clears is then ordered with its kernels."""
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def run(fn, index: int, *args) -> int:
@@ -133,6 +141,10 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     """Writes the new tokens k, v [B, T, kv_heads, d_k] (any strides that are
     multiples of 8 elements, last dimension contiguous) behind each sequence;
     returns new_lens [B] (allocated if not given; not the lens tensor)."""
+    if stream is not None:
+        with on_stream(stream, k_cache):
+            return cache_append(k, v, k_cache, v_cache, page_table, lens, counts, new_lens, acc,
+                                pos, seen, ws)
     c = cache_struct(k_cache, v_cache, page_table, lens)
     index, dt, B = k_cache.get_device(), k_cache.dtype, lens.shape[0]
     if k.dim() != 4:
@@ -151,7 +163,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
              None if acc is None else check(acc, "acc", slots, torch.float32, index),
              None if pos is None else check(pos, "pos", slots, torch.int32, index),
              None if seen is None else check(seen, "seen", (B,), torch.int32, index),
-             ws.data_ptr(), ws.numel(), stream_of(stream, index))
+             ws.data_ptr(), ws.numel(), current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_cache_append")
     return new_lens
@@ -165,6 +177,10 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     """Attention of one new token per sequence, q [B, heads, d_k], over the
     cache; returns out [B, heads, d_k].  With acc, the weight every slot
     received is added: acc_out = acc + weights (acc_out None: in place)."""
+    if stream is not None:
+        with on_stream(stream, k_cache):
+            return attn_decode(q, k_cache, v_cache, page_table, lens, window, sinks, acc, acc_out,
+                               out, ws)
     c = cache_struct(k_cache, v_cache, page_table, lens)
     index, dt, B = k_cache.get_device(), k_cache.dtype, lens.shape[0]
     if q.dim() != 3:
@@ -187,7 +203,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
           else check_workspace(ws, index))
     st = run(_lib.bpt_attn_decode, index, c, qp, h, q.stride(0), q.stride(1), window, sinks, ap,
              aop, op, out.stride(0), out.stride(1), ws.data_ptr(), ws.numel(),
-             stream_of(stream, index))
+             current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_attn_decode")
     return out
@@ -203,6 +219,10 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.
     first ``sinks`` and the last ``recent`` positions and then the largest
     accumulated weights, and packs the rest; returns new_lens.  acc_out,
     pos_out, new_lens None: updated in place."""
+    if stream is not None:
+        with on_stream(stream, k_cache):
+            return cache_evict(k_cache, v_cache, page_table, lens, acc, pos, seen, budget, recent,
+                               sinks, acc_out, pos_out, new_lens, ws)
     c = cache_struct(k_cache, v_cache, page_table, lens)
     index, B = k_cache.get_device(), lens.shape[0]
     slots = (B, k_cache.shape[1], page_table.shape[1] * k_cache.shape[2])
@@ -215,7 +235,7 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.
     st = run(_lib.bpt_cache_evict, index, c, budget, recent, sinks, ap, pp,
              check(seen, "seen", (B,), torch.int32, index), aop, pop,
              check(new_lens, "new_lens", (B,), torch.int32, index), ws.data_ptr(), ws.numel(),
-             stream_of(stream, index))
+             current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_cache_evict")
     return new_lens

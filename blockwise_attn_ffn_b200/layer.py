@@ -11,7 +11,8 @@ import numpy as np
 import torch
 
 from . import _lib
-from .cache import cache_sizes, cache_struct, check, check_workspace, run, stream_of
+from .cache import (cache_sizes, cache_struct, check, check_workspace, current_stream, on_stream,
+                    run)
 
 # Parameter tensors in C-ABI order, with their shapes in terms of (d, d_ff).
 PARAM_NAMES = ["ln1", "W_Q", "W_K", "W_V", "W_O", "ln2", "W_1", "b_1", "W_2", "b_2"]
@@ -256,6 +257,12 @@ def _layer_inputs(x, p):
         if (not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype
                 or t.device != x.device):
             raise ValueError("inputs must be contiguous tensors of one dtype on one GPU")
+    d, d_ff = x.shape[2], p["W_1"].shape[-1]
+    shapes = dict(ln1=(2, d), W_Q=(d, d), W_K=(d, d), W_V=(d, d), W_O=(d, d), ln2=(2, d),
+                  W_1=(d, d_ff), b_1=(d_ff,), W_2=(d_ff, d), b_2=(d,))
+    for k in PARAM_NAMES:
+        if p[k].shape != shapes[k]:
+            raise ValueError(f"{k} must be {list(shapes[k])}, got {list(p[k].shape)}")
     return [t.data_ptr() for t in tensors]
 
 
@@ -276,6 +283,10 @@ def layer_forward_window(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, wi
     ``layer_backward_window`` needs.  cache = (k_cache, v_cache, page_table,
     lens): the tokens' K and V (lens[b] of them, if given) are appended, with
     new_lens [B] int32 (required) and acc, pos, seen as for ``cache_append``."""
+    if stream is not None:
+        with on_stream(stream, x):
+            return layer_forward_window(x, p, h, window, sinks, lens, out, stats, keep_o, cache,
+                                        new_lens, acc, pos, seen, workspace)
     ptrs = _layer_inputs(x, p)
     B, N, d = x.shape
     d_ff = p["W_1"].shape[1]
@@ -299,7 +310,8 @@ def layer_forward_window(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, wi
              opt(keep_o, "keep_o", (B, N, d), torch.float16), c,
              opt(new_lens, "new_lens", (B,), torch.int32), opt(acc, "acc", slots, torch.float32),
              opt(pos, "pos", slots, torch.int32), opt(seen, "seen", (B,), torch.int32),
-             workspace.data_ptr(), workspace.numel(), stream_of(stream, index))
+             check_workspace(workspace, index).data_ptr(), workspace.numel(),
+             current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_layer_forward_window")
     return out, workspace
@@ -312,6 +324,9 @@ def layer_backward_window(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, w
                           stream: Optional[torch.cuda.Stream] = None):
     """Gradients of ``layer_forward_window`` via ``bpt_layer_backward_window``
     (stats and o from it); returns (grads, workspace) as ``layer_backward``."""
+    if stream is not None:
+        with on_stream(stream, x):
+            return layer_backward_window(x, p, h, window, sinks, stats, o, dZ, lens, workspace)
     ptrs = _layer_inputs(x, p)
     B, N, d = x.shape
     d_ff = p["W_1"].shape[1]
@@ -329,8 +344,8 @@ def layer_backward_window(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, w
              check(o, "o", (B, N, d), torch.float16, index),
              check(dZ, "dZ", (B, N, d), torch.float32, index), B, N, d, h, d_ff, code, window,
              sinks, None if lens is None else check(lens, "lens", (B,), torch.int32, index),
-             *[grads[k].data_ptr() for k in GRAD_SHAPES], workspace.data_ptr(), workspace.numel(),
-             stream_of(stream, index))
+             *[grads[k].data_ptr() for k in GRAD_SHAPES], check_workspace(workspace, index).data_ptr(),
+             workspace.numel(), current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_layer_backward_window")
     return grads, workspace
@@ -341,6 +356,9 @@ def layer_decode_workspace(p: Dict[str, torch.Tensor], k_cache: torch.Tensor,
                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """A workspace for ``layer_decode`` steps with these weights (bf16) and a
     cache of these sizes: ``bpt_layer_decode_prepare``, once."""
+    if stream is not None:
+        with on_stream(stream, k_cache):
+            return layer_decode_workspace(p, k_cache, page_table, with_acc)
     c = cache_sizes(k_cache, page_table)
     d, d_ff = p["W_1"].shape
     st, nbytes = _lib.bpt_layer_decode_workspace_size(c, d, d_ff, with_acc)
@@ -351,7 +369,7 @@ def layer_decode_workspace(p: Dict[str, torch.Tensor], k_cache: torch.Tensor,
     shapes = dict(W_Q=(d, d), W_K=(d, d), W_V=(d, d), W_O=(d, d), W_1=(d, d_ff), W_2=(d_ff, d))
     ptrs = [check(p[k], k, s, torch.bfloat16, index) for k, s in shapes.items()]
     st = run(_lib.bpt_layer_decode_prepare, index, *ptrs, c, d, d_ff, with_acc,
-             workspace.data_ptr(), nbytes, stream_of(stream, index))
+             workspace.data_ptr(), nbytes, current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_layer_decode_prepare")
     return workspace
@@ -366,6 +384,10 @@ def layer_decode(x: torch.Tensor, p: Dict[str, torch.Tensor], k_cache: torch.Ten
     """The layer on one new token per sequence, x [B, d] bf16, over an fp16
     cache via ``bpt_layer_decode``; returns (out [B, d] fp32, new_lens).  acc
     is updated in place; new_lens is not the lens tensor: swap the two."""
+    if stream is not None:
+        with on_stream(stream, k_cache):
+            return layer_decode(x, p, k_cache, v_cache, page_table, lens, workspace, window, sinks,
+                                acc, pos, seen, new_lens, out)
     c = cache_struct(k_cache, v_cache, page_table, lens)
     index, B = k_cache.get_device(), lens.shape[0]
     d, d_ff = p["W_1"].shape
@@ -385,7 +407,7 @@ def layer_decode(x: torch.Tensor, p: Dict[str, torch.Tensor], k_cache: torch.Ten
              check(new_lens, "new_lens", (B,), torch.int32, index),
              check(out, "out", (B, d), torch.float32, index),
              check_workspace(workspace, index).data_ptr(), workspace.numel(),
-             stream_of(stream, index))
+             current_stream(index))
     if st != _lib.BPT_OK:
         raise _lib.BptError(st, "bpt_layer_decode")
     return out, new_lens
