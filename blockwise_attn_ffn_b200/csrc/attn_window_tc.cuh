@@ -200,7 +200,11 @@ __device__ __noinline__ void window_row_slow(const WindowParams& p, int b, int h
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
       o[c] = o[c] * alpha + (w == 0.f ? 0.f : w * static_cast<float>(v[j * p.v_n + lane + 32 * c]));
-    if (l != l) break;
+    // a NaN stays: stop once the row can only be NaN
+    bool dead = true;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) dead &= o[c] != o[c];
+    if (l != l || __all_sync(0xFFFFFFFFu, dead)) break;
   }
   T* dst = static_cast<T*>(p.o) + b * p.o_b + i * p.o_n + head * p.o_h;
 #pragma unroll

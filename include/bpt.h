@@ -600,8 +600,9 @@ bpt_status bpt_layer_forward_static(const void* x, const void* ln1, const void* 
  * sequence b is row s % page_size of page page_table[b][s / page_size], for
  * every head; lens[b] slots hold tokens, page_table [batch, max_pages] names
  * the pages of max_pages * page_size slots.  Entries for pages past the
- * sequence's last slot are not read.  A page that two sequences share may be
- * read by both; writing to it (append, evict) through both is undefined.
+ * sequence's last slot are not read.  A page that is named twice, by two
+ * sequences or by one, may be read through both entries; what its rows hold
+ * after writes through both (append, evict) is undefined.
  *
  * State beside the rows, one word per (sequence, kv head, slot), arrays
  * [batch, kv_heads, max_pages * page_size]:
@@ -788,6 +789,7 @@ bpt_status bpt_attn_window_backward(const bpt_window* w, const bpt_rows* q, cons
  * cache (nullable): the sequences' K and V are appended to it (a prompt's
  * prefill: lens are the counts), with new_lens, acc, pos and seen as for
  * bpt_cache_append.  Device errors as for bpt_layer_forward, and BPT_ERR_INDEX.
+ * B = 0 or N = 0: nothing runs, new_lens is not written.
  */
 bpt_status bpt_layer_forward_window_workspace_size(int64_t B, int64_t N, int64_t d, int64_t h,
                                                    int64_t d_ff, bpt_dtype dtype, size_t* bytes);
