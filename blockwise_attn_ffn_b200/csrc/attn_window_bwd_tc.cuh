@@ -13,15 +13,23 @@
 //   window_dkv_tc_kernel  one CTA per 128 keys of a kv head (or a part of
 //                         their queries): K, V stay, the (query head, query
 //                         tile) pairs that see them stream through.
-//   window_join_kernel    adds the parts of blocks that were cut.
 //   window_dq_tc_kernel   one CTA per 128 queries of a head: Q, dO stay, the
 //                         key tiles that they see stream through.
+//   window_join_kernel    adds the parts of blocks that were cut.
 // 7 products of 2 d_k flops per pair for the 5 of the formulas: S and dP are
 // computed twice, which keeps dQ out of memory and results independent of
-// timing.  Measured at 16384 tokens, 16 heads of 128 on 4, window 2048: 0.90 ms in
-// bursts, of which dK/dV 505 us (3000 clocks per 128 x 128 step for 2048 of
+// timing.  Measured at 16384 tokens, 16 heads of 128 on 4, window 2048: 0.86 ms in
+// bursts; alone, dK/dV take 505 us (3000 clocks per 128 x 128 step for 2048 of
 // products: P, dV and the next scores, which go where P lies, follow one
 // another), dQ 409, terms 31.
+//
+// The launches overlap (programmatic launches).  dK/dV blocks do all but the
+// row terms while the last terms are written.  dQ needs the terms, not dK/dV:
+// it may start once every dK/dV block has, and its short blocks fill the SMs
+// that the last, long dK/dV blocks leave idle.  Its last block waits for the
+// dK/dV grid before it ends, so that whatever follows finds both done.  One
+// launch after the other measured 896 us against 859, and 139 against 116 us for
+// eight ragged sequences of up to 2048 tokens, 12 heads of 64, window 256.
 //
 // Query tiles of a key block END at the last valid query that sees it, key
 // tiles of a query block at its last visible key: nothing past a sequence's
@@ -87,6 +95,17 @@ struct WindowBwdParams {
   uint32_t* err;
 };
 
+// Launches that follow one another in a stream may overlap (programmatic
+// launches): a grid starts once every block of the one before it has signalled
+// (or ended), and waits where it needs that grid's results, which are complete
+// and visible behind the wait.  No wait without such a launch: returns at once.
+__device__ __forceinline__ void grid_signal() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Query tiles that see the 128 keys from kb, of queries before row `limit`.
 struct WindowQueries {
   int start, end;  // rows; tiles end at `end`
@@ -116,7 +135,7 @@ struct WinScale {
 // 2^-e with max |dO| in [2^e, 2^(e+1)); 1 where that is no use.
 __device__ __forceinline__ float grad_sigma(const uint32_t* amax) {
   if (amax == nullptr) return 1.f;
-  const uint32_t e = __ldg(amax) >> 23;  // biased exponent (the sign is 0)
+  const uint32_t e = __ldcg(amax) >> 23;  // biased exponent (the sign is 0)
   if (e == 0 || e >= 250) return 1.f;
   return __uint_as_float((254u - e) << 23);
 }
@@ -142,6 +161,7 @@ constexpr int kTermRows = 4;  // rows per group of lanes, their loads in flight 
 // consecutive groups read on.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) window_terms_kernel(const WindowTermsParams p) {
+  grid_signal();
   constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
   // the block's first row: one 64-bit division for all
   const long long r0 = static_cast<long long>(blockIdx.x) * (kGroups * kTermRows);
@@ -534,6 +554,8 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     mbar_wait_drain(drain, 0, p.err);
   } else if (warp == 3) {
     // ----------------------------------------------------------- row terms
+    grid_wait();
+    grid_signal();  // (behind the wait: the dQ blocks read the terms too)
     const float sig = grad_sigma(p.amax) * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
     const float2* rows = p.terms + (static_cast<long long>(bidx) * p.h + kvh * p.g + hl0) * p.nq;
     int tl = tl0;
@@ -543,7 +565,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
 #pragma unroll
       for (int q = 0; q < C::QT / 32; ++q) {
         const int i = t0 + C::QT * tl + lane + 32 * q;
-        v[q] = i >= 0 ? __ldg(rows + i) : make_float2(-INFINITY, 0.f);
+        v[q] = i >= 0 ? __ldcg(rows + i) : make_float2(-INFINITY, 0.f);
       }
       if (!mbar_wait_warp(terms_empty0 + 8 * ts,
                           static_cast<uint32_t>((t / C::TERM_SLOTS) & 1) ^ 1u, abort_flag, p.err,
@@ -564,6 +586,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------- elementwise
+    grid_wait();  // max |dO|
     const int e = warp & 3, cc = (warp - 4) >> 2;  // columns 32 cc ..
     const int kr = e * 32 + lane, key = kb + kr;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
@@ -673,6 +696,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
 // parts added in order.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) window_join_kernel(const WindowBwdParams p) {
+  grid_wait();
   const int bk = blockIdx.y, bidx = bk / p.hkv, kvh = bk - bidx * p.hkv;
   const int which = blockIdx.z & 1, quarter = blockIdx.z >> 1;
   int len = p.lens != nullptr ? __ldg(p.lens + bidx) : p.nkv;
@@ -898,7 +922,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     const float sigma = grad_sigma(p.amax);
     const float sig = sigma * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
     float2 tr = make_float2(-INFINITY, 0.f);
-    if (i < p.nq) tr = __ldg(p.terms + (static_cast<long long>(bidx) * p.h + head) * p.nq + i);
+    if (i < p.nq) tr = __ldcg(p.terms + (static_cast<long long>(bidx) * p.h + head) * p.nq + i);
     const float2 a2 = make_float2(tr.x, tr.x), nd2 = make_float2(tr.y * sig, tr.y * sig);
     auto term = [&](int) { return a2; };
     auto nd = [&](int) { return nd2; };
@@ -966,6 +990,9 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, C::COLS);
+  // the grid ends behind the dK/dV grid, for what follows in the stream
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+    grid_wait();
 }
 
 }  // namespace bpt

@@ -365,6 +365,24 @@ bpt_status check_window_bwd(const bpt_window* w) {
   return BPT_OK;
 }
 
+// A launch that may start before the one in front of it has ended (the kernel
+// waits where it has to).
+template <typename K, typename... A>
+cudaError_t launch_early(K kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename T, int D>
 cudaError_t launch_window_bwd(const CUtensorMap* stay, const CUtensorMap* stream,
                               const bpt::WindowTermsParams& tp,
@@ -374,16 +392,20 @@ cudaError_t launch_window_bwd(const CUtensorMap* stay, const CUtensorMap* stream
   const int64_t rows = int64_t(p.nq) * p.h, per = 256 / (D / 8) * bpt::kTermRows;
   bpt::window_terms_kernel<T, D>
       <<<dim3(unsigned((rows + per - 1) / per), unsigned(batch)), 256, 0, s>>>(tp);
-  bpt::window_dkv_tc_kernel<T, D>
-      <<<dim3(unsigned(plan.parts), unsigned(batch * p.hkv)), bpt::kWinBwdThreads<D>, C::KV_SMEM,
-         s>>>(stream[0], stay[1], stay[2], stream[3], p);
-  if (plan.cut_blocks > 0)
-    bpt::window_join_kernel<T, D>
-        <<<dim3(unsigned(plan.cut_blocks), unsigned(batch * p.hkv), 8), 256, 0, s>>>(p);
-  bpt::window_dq_tc_kernel<T, D>
-      <<<dim3(unsigned(p.nqb), unsigned(p.h), unsigned(batch)), bpt::kWinBwdThreads<D>, C::Q_SMEM,
-         s>>>(stay[0], stream[1], stream[2], stay[3], p);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // dK/dV start on their products while the last terms are written; dQ's blocks,
+  // which need the terms alone, fill the SMs that the last dK/dV blocks leave
+  e = launch_early(bpt::window_dkv_tc_kernel<T, D>,
+                   dim3(unsigned(plan.parts), unsigned(batch * p.hkv)), bpt::kWinBwdThreads<D>,
+                   C::KV_SMEM, s, stream[0], stay[1], stay[2], stream[3], p);
+  if (e != cudaSuccess) return e;
+  e = launch_early(bpt::window_dq_tc_kernel<T, D>,
+                   dim3(unsigned(p.nqb), unsigned(p.h), unsigned(batch)), bpt::kWinBwdThreads<D>,
+                   C::Q_SMEM, s, stay[0], stream[1], stream[2], stay[3], p);
+  if (e != cudaSuccess || plan.cut_blocks == 0) return e;
+  return launch_early(bpt::window_join_kernel<T, D>,
+                      dim3(unsigned(plan.cut_blocks), unsigned(batch * p.hkv), 8), 256, 0, s, p);
 }
 
 }  // namespace
