@@ -18,7 +18,7 @@
 //   window_join_kernel    adds the parts of blocks that were cut.
 // 7 products of 2 d_k flops per pair for the 5 of the formulas: S and dP are
 // computed twice, which keeps dQ out of memory and results independent of
-// timing.  Measured at 16384 tokens, 16 heads of 128 on 4, window 2048: 0.86 ms in
+// timing.  Measured at 16384 tokens, 16 heads of 128 on 4, window 2048: 0.84 ms in
 // bursts; alone, dK/dV take 505 us (3000 clocks per 128 x 128 step for 2048 of
 // products: P, dV and the next scores, which go where P lies, follow one
 // another), dQ 409, terms 31.
@@ -28,8 +28,9 @@
 // it may start once every dK/dV block has, and its short blocks fill the SMs
 // that the last, long dK/dV blocks leave idle.  Its last block waits for the
 // dK/dV grid before it ends, so that whatever follows finds both done.  One
-// launch after the other measured 896 us against 859, and 139 against 116 us for
-// eight ragged sequences of up to 2048 tokens, 12 heads of 64, window 256.
+// launch after the other took 896 us instead of 859, and 139 instead of 116 for
+// eight ragged sequences of up to 2048 tokens, 12 heads of 64, window 256 (both
+// with the rows stored as the lanes hold them; 841 and 100 since).
 //
 // Query tiles of a key block END at the last valid query that sees it, key
 // tiles of a query block at its last visible key: nothing past a sequence's
@@ -646,43 +647,51 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     }
     const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
     tc_fence_after();
-    // even column groups store dV, odd ones dK, sharing the d_k / 32 pieces
-    const int half = cc & 1;
+    // even column groups store dV, odd ones dK, 64 columns each
+    const int half = cc & 1, c0 = 64 * (cc >> 1);
     const float f = half == 0 ? exp2f(-WinScale<T>::kP) : p.scale / (sigma * WinScale<T>::kDS);
     const uint32_t acc = t_lane + (half == 0 ? C::TM_DV : C::TM_DK);
     if (slot0 >= 0) {
       if (done) {  // (a part without items writes nothing and is not read)
+        // four columns of all 128 rows lie together: a warp writes 512 bytes at once
         float* dst = p.part + ((static_cast<long long>(bk) * p.split_parts + slot0 + part) * 2 + half) *
-                                  (128 * D) + kr * D;
+                                  (128 * D) + kr * 4;
 #pragma unroll 1
-        for (int x = cc >> 1; x < D / 32; x += C::QT / 64) {
+        for (int x = c0; x < c0 + 64; x += 32) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(acc + x * 32, v);
+          tmem_ld_32x32b_x32(acc + x, v);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(dst + x * 32 + k) =
+            *reinterpret_cast<float4*>(dst + (x + k) * 128) =
                 make_float4(__uint_as_float(v[k]) * f, __uint_as_float(v[k + 1]) * f,
                             __uint_as_float(v[k + 2]) * f, __uint_as_float(v[k + 3]) * f);
         }
       }
     } else {
-      T* dst = half == 0
-                   ? static_cast<T*>(p.dv) + bidx * p.dv_b + key * p.dv_n + kvh * p.dv_h
-                   : static_cast<T*>(p.dk) + bidx * p.dk_b + key * p.dk_n + kvh * p.dk_h;
+      // (staged where the queries were: every product is done)
+      static_assert(kWinElemWarps<D> * 4096 <= C::Q_SLOTS * C::STREAM, "staging");
+      uint8_t* st = smem + C::KV_OFF_Q + (warp - 4) * 4096;
 #pragma unroll 1
-      for (int x = cc >> 1; x < D / 32; x += C::QT / 64) {
+      for (int x = 0; x < 8 && done; x += 4) {
         uint32_t v[32];
-        if (done) {
-          tmem_ld_32x32b_x32(acc + x * 32, v);
-          tmem_ld_wait();
-        }
-        if (key >= p.nkv) continue;
-        const bool zero = !done || key >= len;  // no query sees the key
+        tmem_ld_32x32b_x32(acc + c0 + x * 8, v);
+        tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 32; k += 8)
-          *reinterpret_cast<uint4*>(dst + x * 32 + k) =
-              zero ? make_uint4(0u, 0u, 0u, 0u) : win_pack8<T>(v + k, f);
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(st + stage_at<8>(lane, x + k)) = win_pack8<T>(v + 8 * k, f);
+      }
+      __syncwarp();
+      T* dst = half == 0 ? static_cast<T*>(p.dv) + bidx * p.dv_b + kvh * p.dv_h
+                         : static_cast<T*>(p.dk) + bidx * p.dk_b + kvh * p.dk_h;
+      const long long dn = half == 0 ? p.dv_n : p.dk_n;
+#pragma unroll 4
+      for (int x = lane >> 3; x < 32; x += 4) {
+        const int row = kb + e * 32 + x;
+        if (row < p.nkv)  // (keys from the length on: no query sees them)
+          *reinterpret_cast<uint4*>(dst + row * dn + c0 + (lane & 7) * 8) =
+              done && row < len ? *reinterpret_cast<const uint4*>(st + stage_at<8>(x, lane & 7))
+                                : make_uint4(0u, 0u, 0u, 0u);
       }
     }
   }
@@ -716,14 +725,14 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WindowBwdParams 
   const float* src = p.part + (static_cast<long long>(bk) * p.split_parts + slot) * (2 * 128 * D) +
                      which * (128 * D);
   for (int x = threadIdx.x; x < 32 * D / 8; x += 256) {
-    const int kr = quarter * 32 + x / (D / 8), col = x % (D / 8) * 8, key = blk * 128 + kr;
+    const int kr = quarter * 32 + x % 32, col = x / 32 * 8, key = blk * 128 + kr;
     if (key >= p.nkv) continue;
     float a[8] = {};
     if (key < len)
       for (int q = 0; q < parts; ++q) {
         const float4* s = reinterpret_cast<const float4*>(src + static_cast<long long>(q) * (2 * 128 * D) +
-                                                          kr * D + col);
-        const float4 u = s[0], v = s[1];
+                                                          col * 128) + kr;
+        const float4 u = s[0], v = s[128];
         a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
         a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
       }
@@ -970,20 +979,27 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
     tc_fence_after();
     const float f = p.scale / (sigma * WinScale<T>::kDS);
-    T* dst = static_cast<T*>(p.dq) + bidx * p.dq_b + i * p.dq_n + head * p.dq_h;
-    // the column groups share the d_k / 32 pieces of the row
-    for (int x = cc; x < D / 32; x += C::QT / 32) {
+    // 32 columns per warp, staged where the keys were: every product is done
+    static_assert(D / 32 == C::QT / 32, "a column group per warp");
+    static_assert(kWinElemWarps<D> * 2048 <= C::QK_SLOTS * C::STREAM, "staging");
+    uint8_t* st = smem + C::Q_OFF_K + (warp - 4) * 2048;
+    if (done) {
       uint32_t v[32];
-      if (done) {
-        tmem_ld_32x32b_x32(t_lane + C::TQ_A + x * 32, v);
-        tmem_ld_wait();
-      }
-      if (i >= p.nq) continue;
-      const bool zero = !done || pos >= len;
+      tmem_ld_32x32b_x32(t_lane + C::TQ_A + cc * 32, v);
+      tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 32; k += 8)
-        *reinterpret_cast<uint4*>(dst + x * 32 + k) =
-            zero ? make_uint4(0u, 0u, 0u, 0u) : win_pack8<T>(v + k, f);
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(st + stage_at<4>(lane, k)) = win_pack8<T>(v + 8 * k, f);
+    }
+    __syncwarp();
+    T* dst = static_cast<T*>(p.dq) + bidx * p.dq_b + head * p.dq_h + cc * 32;
+#pragma unroll
+    for (int x = lane >> 2; x < 32; x += 8) {
+      const int row = qb * 128 + e * 32 + x;
+      if (row < p.nq)
+        *reinterpret_cast<uint4*>(dst + row * p.dq_n + (lane & 3) * 8) =
+            done && off + row < len ? *reinterpret_cast<const uint4*>(st + stage_at<4>(x, lane & 3))
+                                    : make_uint4(0u, 0u, 0u, 0u);
     }
   }
   tc_fence_before();
