@@ -620,7 +620,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
 }
 
 constexpr int kWeightThreads = 256;
-constexpr int kWeightSlots = 2048;  // slots per block
+// Slots per block, four per thread.  Eight per thread: the same for 64 sequences
+// (266 us with the attention), 92 us instead of 86 for 16.
+constexpr int kWeightSlots = 4 * kWeightThreads;
 
 // Grid (slot blocks, h_kv, B): acc_out = acc + the weight each slot received,
 // from the saved scores and the joined (m, l).
@@ -641,29 +643,26 @@ __global__ void __launch_bounds__(kWeightThreads) attn_decode_weights_kernel(con
   const long long a0 = (static_cast<long long>(b) * p.c.hkv + kvh) * p.c.cap;
   const float* sc = p.scores + (static_cast<long long>(b) * p.h + kvh * p.g) * p.scores_ld;
   const uint32_t first = blockIdx.x * kWeightSlots + tid;
-  // four slots at a time, their loads independent
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWeightSlots / kWeightThreads; i += 4) {
-    float w[4] = {}, old[4];
-    const float* at[4];
+  // (the loads of a thread's slots are independent)
+  float w[4] = {}, old[4];
+  const float* at[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t s = first + (i + x) * kWeightThreads;
-      const bool seen = s < sq.len && (s >= sq.lo || s < sq.ns);
-      at[x] = seen ? sc + (s < sq.ns ? s : sq.ns + (s - sq.lo)) : nullptr;
-      old[x] = s < sq.len ? p.acc[a0 + s] : 0.f;
-    }
-    for (uint32_t r = 0; r < p.g; ++r) {
-      const float2 ml = ml_sh[r];
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t s = first + x * kWeightThreads;
+    const bool seen = s < sq.len && (s >= sq.lo || s < sq.ns);
+    at[x] = seen ? sc + (s < sq.ns ? s : sq.ns + (s - sq.lo)) : nullptr;
+    old[x] = s < sq.len ? p.acc[a0 + s] : 0.f;
+  }
+  for (uint32_t r = 0; r < p.g; ++r) {
+    const float2 ml = ml_sh[r];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (at[x] != nullptr) w[x] += ex2_approx(at[x][r * p.scores_ld] - ml.x) * ml.y;
-    }
+    for (int x = 0; x < 4; ++x)
+      if (at[x] != nullptr) w[x] += ex2_approx(at[x][r * p.scores_ld] - ml.x) * ml.y;
+  }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t s = first + (i + x) * kWeightThreads;
-      if (s < sq.len) p.acc_out[a0 + s] = old[x] + w[x];
-    }
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t s = first + x * kWeightThreads;
+    if (s < sq.len) p.acc_out[a0 + s] = old[x] + w[x];
   }
 }
 
