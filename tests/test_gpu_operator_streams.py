@@ -125,3 +125,45 @@ def test_a_row_of_nothing_but_nan_stays_so():
     assert bad[:, 100:500, :, 7].all()
     bad[:, 100:500, :, 7] = False
     assert not bad.any()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_gradients_one_after_another_through_one_workspace(captured):
+    """The launches of a call overlap; those of the next call, and whatever
+    reads the gradients, find all of them done: bitwise what each call gives
+    alone."""
+    calls = []
+    for i, (B, n, h, hkv, dk, window, sinks, dt) in enumerate([
+            (3, 700, 4, 2, 64, 100, 4, BF), (1, 2100, 4, 1, 128, 300, 130, torch.float16),
+            (2, 60, 2, 2, 64, 64, 0, torch.float16), (1, 1500, 2, 2, 128, 1500, 0, BF)]):
+        q, do = tensors(20 + i, (B, n, h, dk), (B, n, h, dk), dt=dt)
+        k, v = tensors(30 + i, (B, n, hkv, dk), (B, n, hkv, dk), dt=dt)
+        lens = torch.tensor([n - 37 * b for b in range(B)], dtype=torch.int32, device="cuda")
+        stats = torch.empty((B, h, n, 2), device="cuda")
+        o = bpt.attn_window_forward(q, k, v, window, sinks, lens=lens, stats=stats)
+        want = bpt.attn_window_backward(q, k, v, o, stats, do, window, sinks, lens=lens)
+        torch.cuda.synchronize()
+        calls.append(((q, k, v, o, stats, do, window, sinks, lens), want))
+    ws = max((bpt.attn_window_backward_workspace(a[0], a[1], a[6], a[7]) for a, _ in calls),
+             key=torch.Tensor.numel)
+    grads = [[torch.empty_like(w) for w in want] for _, want in calls]
+    copies = [[torch.empty_like(w) for w in want] for _, want in calls]
+
+    def every():
+        for (args, _), into, copy in zip(calls, grads, copies):
+            bpt.attn_window_backward(*args, into, ws)
+            for c, g in zip(copy, into):
+                c.copy_(g)
+
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            every()
+    for _ in range(10):
+        for c in sum(copies, []):
+            c.zero_()
+        graph.replay() if captured else every()
+        for (_, want), copy in zip(calls, copies):
+            for w, c in zip(want, copy):
+                assert torch.equal(w, c)
