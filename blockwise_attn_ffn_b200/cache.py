@@ -10,7 +10,8 @@ defines what they compute.  A cache is four tensors that the program keeps:
 
 and, where weights are gathered for eviction, acc (fp32) and pos (int32),
 both [B, kv_heads, max_pages * page_size].  Lengths and pages stay on the
-device: no call synchronises, and every call may be captured into a graph.
+device: no call synchronises, and every call may be captured into a graph.  With
+``stream=`` a call runs with that stream current: what it allocates belongs to it.
 """
 from __future__ import annotations
 

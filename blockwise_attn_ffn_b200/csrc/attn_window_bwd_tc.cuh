@@ -455,6 +455,9 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
         const int qs = t % C::Q_SLOTS, ds = t % C::DO_SLOTS;
         const uint32_t qph = static_cast<uint32_t>((t / C::Q_SLOTS) & 1);
         const uint32_t dph = static_cast<uint32_t>((t / C::DO_SLOTS) & 1);
+        // (the rings are full: what empties them waits for the terms, however
+        // long that takes, so the bounded waits start behind it)
+        if (t == C::DO_SLOTS) grid_wait();
         if (!mbar_wait_warp(q_empty0 + 8 * qs, qph ^ 1u, abort_flag, p.err, kSiteAttnProducer))
           break;
         q_armed[qs] = static_cast<int>(qph);
@@ -536,6 +539,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     };
     bool ok = n_it > 0 && mbar_wait_warp(kv_full, 0, abort_flag, p.err, kSiteAttnMma) &&
               issue_s(0) && issue_dp(0);
+    grid_wait();  // (as above: P comes behind the terms)
     for (int t = 0; t < n_it && ok; ++t) {
       // dV += P^T dO_t; then S^T_t has been read in full: the next scores go there
       if (!(ok = issue_grad(t, p_half0, tmem + C::TM_DV, tmem + C::TM_S,
