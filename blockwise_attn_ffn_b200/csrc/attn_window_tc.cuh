@@ -35,6 +35,9 @@
 // ms: the exponentials of a tile keep the scheduler's unit busy as long, and the
 // exchange comes on top.
 //
+// A score that is NaN or +inf makes its row NaN.  The cubic exponential would
+// lose it (its clamp turns NaN into a weight of 2^-125), so the row maximum
+// keeps NaN and a maximum that is not below +inf spoils the row's sum.
 // A masked key has weight 0, but 0 x V_j is NaN if V_j holds NaN or infinity.
 // Rows whose result is not finite are therefore done again, key by key over
 // what they see (window_row_slow): exact, and free for finite values.
@@ -178,6 +181,13 @@ __device__ __forceinline__ uint32_t window_bits(int p, int kb, int lo, int windo
   const int top = p - kb + 1, low = lo - kb;
   return bits_range(max(p - window + 1 - kb, low), top, w) |
          bits_range(low, min(sinks - kb, top), w);
+}
+
+// The largest of three values, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
 }
 
 // One row over its visible keys, by a warp: fp32, key by key, online softmax.
@@ -490,11 +500,12 @@ __global__ void __launch_bounds__(384, 1)
       for (int k = 0; k < 128; k += 16)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          mxp[q] = fmaxf(fmaxf(mxp[q], __uint_as_float(sr[k + q])), __uint_as_float(sr[k + 8 + q]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mxp[k] = fmaxf(mxp[k], mxp[k + 4]);
-      const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
-      m_true = fmaxf(m_true, mx);
+          mxp[q] = max3_nan(mxp[q], __uint_as_float(sr[k + q]), __uint_as_float(sr[k + 8 + q]));
+      mxp[0] = max3_nan(mxp[0], mxp[1], mxp[2]);
+      mxp[3] = max3_nan(mxp[3], mxp[4], mxp[5]);
+      const float mx = max3_nan(mxp[0], mxp[3], max3_nan(mxp[6], mxp[7], mxp[7]));
+      m_true = max3_nan(m_true, mx, mx);
+      const float spoil = mx < INFINITY ? 0.f : __uint_as_float(0x7FC00000u);
       float m_new = m_run;
       bool need = false;
       if (mx > m_run) {
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(384, 1)
       else
         exp_row(std::integral_constant<uint32_t, 0u>{});
       sum2[0] = __fadd2_rn(__fadd2_rn(sum2[0], sum2[1]), __fadd2_rn(sum2[2], sum2[3]));
-      l = alpha * l + (sum2[0].x + sum2[0].y);
+      l = alpha * l + (sum2[0].x + sum2[0].y) + spoil;
       m_run = m_new;
       o_live = true;
     }

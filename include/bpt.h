@@ -720,7 +720,8 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
  * broadcast dimension (stride 0) is refused with BPT_ERR_INVALID_ARG.
  *
  * Only what a row sees counts: NaN and infinities in keys and values that it
- * does not see (masked ones, padding) do not reach its output.
+ * does not see (masked ones, padding) do not reach its output.  A score of NaN
+ * or +inf that it does see makes its output and its l NaN, as in a softmax.
  *
  * Workspaces: as for the cache's operators.
  */
