@@ -9,7 +9,8 @@
 //
 // Four launches, all sums in a fixed order (no atomics on results):
 //   window_terms_kernel   per row a' = -(m + ln l) log2 e and -D (reads o, dO
-//                         once); for fp16 also max |dO|.
+//                         once); for fp16 also the largest norms of rows of dO
+//                         and V (reads V once).
 //   window_dkv_tc_kernel  one CTA per 128 keys of a kv head (or a part of
 //                         their queries): K, V stay, the (query head, query
 //                         tile) pairs that see them stream through.
@@ -42,9 +43,13 @@
 // accumulators and the join adds them in order.
 //
 // Rounding: P and dS are rounded to the operands' type for the products.
-// fp16 has 5 exponent bits, so there both are scaled by powers of two (exact):
-// P by 2^8, dS by 2^4 over max |dO| (its exponent), which keeps weights down
-// to 2^-22 and gradients 2^-40 below the largest out of the subnormals.
+// fp16 has 5 exponent bits, so there both are scaled by powers of two (exact).
+// P by 2^8: weights down to 2^-22 stay out of the subnormals.  dS by what its
+// range allows: |dP - D| <= 2 R with R = max |dO_i| max |v_j| (2-norms) over the
+// rows of a (sequence, kv head), and the scale, between 2^13 / R and 2^14 / R,
+// leaves |dS| below 2^15 for any finite values, and out of the subnormals down
+// to 2^-27 R (an absolute error of 2^-38 R below that).  Sequences and kv heads
+// have scales of their own: none loses bits to a neighbour.
 #pragma once
 
 #include <type_traits>
@@ -82,7 +87,7 @@ struct WindowBwdParams {
   int window, sinks;
   const int* lens;        // nullable [B]
   const float2* terms;    // [B][h][nq]: (a', -D); (-inf, 0) past the length
-  const uint32_t* amax;   // fp16: bits of max |dO|; null: bf16
+  const uint2* range;     // fp16: [B][hkv] largest squared norms of dO's and V's rows; null: bf16
   void* dq;
   long long dq_b, dq_n, dq_h;
   void* dk;
@@ -130,15 +135,18 @@ __host__ __device__ inline int window_parts(int nq, int nkv, int window, int sin
 
 template <typename T>
 struct WinScale {
-  static constexpr float kP = std::is_same<T, __half>::value ? 8.f : 0.f;     // log2 of P's scale
-  static constexpr float kDS = std::is_same<T, __half>::value ? 16.f : 1.f;   // dS's, over max |dO|
+  static constexpr float kP = std::is_same<T, __half>::value ? 8.f : 0.f;  // log2 of P's scale
 };
-// 2^-e with max |dO| in [2^e, 2^(e+1)); 1 where that is no use.
-__device__ __forceinline__ float grad_sigma(const uint32_t* amax) {
-  if (amax == nullptr) return 1.f;
-  const uint32_t e = __ldcg(amax) >> 23;  // biased exponent (the sign is 0)
-  if (e == 0 || e >= 250) return 1.f;
-  return __uint_as_float((254u - e) << 23);
+// dS's scale: the power of two s with 2^13 <= s R < 2^14, R^2 the product of the
+// two squared norms; 1 where that is no use (R = 0, or not finite).
+__device__ __forceinline__ float grad_scale(const uint2* range, long long pair) {
+  if (range == nullptr) return 1.f;
+  const uint2 v = __ldcg(range + pair);
+  const uint32_t e = __float_as_uint(__uint_as_float(v.x) * __uint_as_float(v.y)) >> 23;
+  if (e == 0 || e >= 255) return 1.f;
+  // R^2 in [2^(e - 127), 2^(e - 126)), R in [2^h, 2^(h + 1)) with h = floor((e - 127) / 2)
+  const int h = (static_cast<int>(e) - 127) >> 1;
+  return __uint_as_float(static_cast<uint32_t>(127 + 13 - h) << 23);
 }
 
 // ------------------------------------------------------------------- terms --
@@ -147,75 +155,113 @@ struct WindowTermsParams {
   long long o_b, o_n, o_h;
   const void* d_o;
   long long d_b, d_n, d_h;
+  const void* v;
+  long long v_b, v_n, v_h;
   const float2* stats;  // [B][h][nq]
   float2* terms;
-  uint32_t* amax;       // nullable
+  uint32_t* range;      // nullable [B][hkv][2], zeros: see WindowBwdParams
   const int* lens;
-  int B, nq, nkv, h;
+  int nq, nkv, h, g;    // g = h / hkv
+  uint32_t row_blocks;  // blocks of rows; those behind them have rows of V
   uint32_t* err;
 };
 
 constexpr int kTermRows = 4;  // rows per group of lanes, their loads in flight together
+template <int D>
+constexpr int kTermBlockRows = 256 / (D / 8) * kTermRows;
 
-// Grid (blocks of one sequence's rows, B): D / 8 lanes per row (16 bytes of o
-// and dO each), rows in (i, head) order, a block's rows one group apart so that
-// consecutive groups read on.
+// Grid (blocks of one kv head's rows, hkv, B): D / 8 lanes per row (16 bytes of
+// o and dO each), rows in (i, head of the group) order, a block's rows one group
+// apart so that consecutive groups read on.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) window_terms_kernel(const WindowTermsParams p) {
   grid_signal();
   constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
-  // the block's first row: one 64-bit division for all
-  const long long r0 = static_cast<long long>(blockIdx.x) * (kGroups * kTermRows);
-  const int i0 = static_cast<int>(r0 / p.h), t0 = static_cast<int>(r0 - static_cast<long long>(i0) * p.h);
-  const int b = blockIdx.y;
+  constexpr bool kRange = std::is_same<T, __half>::value;
+  const int kvh = blockIdx.y, b = blockIdx.z;
   int len = p.lens != nullptr ? __ldg(p.lens + b) : p.nkv;
   if (len < 0 || len > p.nkv) {
     if (threadIdx.x == 0) record_error(p.err, kErrIndex, kSiteWindowLens);
     len = len < 0 ? 0 : p.nkv;
   }
-  const int lane = threadIdx.x % kLanes;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  float mx = 0.f;  // the largest squared norm of this block's rows (of dO, or of V)
   uint4 a[kTermRows], c[kTermRows];
-  float2 ml[kTermRows];
-  long long at[kTermRows];  // index into stats and terms; -1: no row
   bool valid[kTermRows];
+  const bool values = kRange && blockIdx.x >= p.row_blocks;
+  if (!values) {
+    // the block's first row: one 64-bit division for all
+    const long long r0 = static_cast<long long>(blockIdx.x) * kTermBlockRows<D>;
+    const int i0 = static_cast<int>(r0 / p.g), t0 = static_cast<int>(r0 - static_cast<long long>(i0) * p.g);
+    float2 ml[kTermRows];
+    long long at[kTermRows];  // index into stats and terms; -1: no row
 #pragma unroll
-  for (int u = 0; u < kTermRows; ++u) {
-    const uint32_t x = t0 + threadIdx.x / kLanes + u * kGroups;
-    const int i = i0 + static_cast<int>(x / static_cast<uint32_t>(p.h));
-    const int t = static_cast<int>(x % static_cast<uint32_t>(p.h));
-    at[u] = i < p.nq ? (static_cast<long long>(b) * p.h + t) * p.nq + i : -1;
-    valid[u] = i < p.nq && p.nkv - p.nq + i < len;
-    if (valid[u]) {
-      a[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + b * p.o_b +
-                                                  i * p.o_n + t * p.o_h) + lane);
-      c[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.d_o) + b * p.d_b +
-                                                  i * p.d_n + t * p.d_h) + lane);
-      if (lane == 0) ml[u] = __ldg(p.stats + at[u]);
-    }
-  }
-  float mx = 0.f;
-#pragma unroll
-  for (int u = 0; u < kTermRows; ++u) {
-    float sum = 0.f;
-    if (valid[u]) {
-      const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
-      const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = unpack16<T>(aw[k]), y = unpack16<T>(cw[k]);
-        sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
-        mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
+    for (int u = 0; u < kTermRows; ++u) {
+      const uint32_t x = t0 + group + u * kGroups;
+      const int i = i0 + static_cast<int>(x / static_cast<uint32_t>(p.g));
+      const int t = kvh * p.g + static_cast<int>(x % static_cast<uint32_t>(p.g));
+      at[u] = i < p.nq ? (static_cast<long long>(b) * p.h + t) * p.nq + i : -1;
+      valid[u] = i < p.nq && p.nkv - p.nq + i < len;
+      if (valid[u]) {
+        a[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + b * p.o_b +
+                                                    i * p.o_n + t * p.o_h) + lane);
+        c[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.d_o) + b * p.d_b +
+                                                    i * p.d_n + t * p.d_h) + lane);
+        if (lane == 0) ml[u] = __ldg(p.stats + at[u]);
       }
     }
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (at[u] >= 0 && lane == 0) {
-      p.terms[at[u]] = valid[u] && ml[u].y > 0.f
-                           ? make_float2(-(ml[u].x + logf(ml[u].y)) * kLog2e + WinScale<T>::kP, -sum)
-                           : make_float2(-INFINITY, 0.f);
+    for (int u = 0; u < kTermRows; ++u) {
+      float sum = 0.f, norm = 0.f;
+      if (valid[u]) {
+        const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+        const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = unpack16<T>(aw[k]), y = unpack16<T>(cw[k]);
+          sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+          if constexpr (kRange) norm = fmaf(y.x, y.x, fmaf(y.y, y.y, norm));
+        }
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if constexpr (kRange) norm += __shfl_xor_sync(0xffffffffu, norm, o);
+      }
+      mx = fmaxf(mx, norm);
+      if (at[u] >= 0 && lane == 0) {
+        p.terms[at[u]] = valid[u] && ml[u].y > 0.f
+                             ? make_float2(-(ml[u].x + logf(ml[u].y)) * kLog2e + WinScale<T>::kP, -sum)
+                             : make_float2(-INFINITY, 0.f);
+      }
+    }
+  } else {
+    const long long j0 = static_cast<long long>(blockIdx.x - p.row_blocks) * kTermBlockRows<D>;
+#pragma unroll
+    for (int u = 0; u < kTermRows; ++u) {
+      const long long j = j0 + group + u * kGroups;
+      valid[u] = j < len;
+      if (valid[u])
+        c[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + b * p.v_b +
+                                                    j * p.v_n + kvh * p.v_h) + lane);
+    }
+#pragma unroll
+    for (int u = 0; u < kTermRows; ++u) {
+      float norm = 0.f;
+      if (valid[u]) {
+        const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 y = unpack16<T>(cw[k]);
+          norm = fmaf(y.x, y.x, fmaf(y.y, y.y, norm));
+        }
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, o);
+      mx = fmaxf(mx, norm);
     }
   }
-  if (p.amax != nullptr) {
+  if constexpr (kRange) {
     __shared__ uint32_t mx_sh[8];
     const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
     if ((threadIdx.x & 31) == 0) mx_sh[threadIdx.x >> 5] = w;
@@ -223,7 +269,9 @@ __global__ void __launch_bounds__(256) window_terms_kernel(const WindowTermsPara
     if (threadIdx.x == 0) {
       uint32_t m = 0;
       for (int k = 0; k < 8; ++k) m = max(m, mx_sh[k]);
-      if (m != 0) atomicMax(p.amax, m);  // a maximum: the same in any order
+      // (a maximum: the same in any order)
+      if (m != 0)
+        atomicMax(p.range + (static_cast<long long>(b) * gridDim.y + kvh) * 2 + (values ? 1 : 0), m);
     }
   }
 }
@@ -561,7 +609,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     // ----------------------------------------------------------- row terms
     grid_wait();
     grid_signal();  // (behind the wait: the dQ blocks read the terms too)
-    const float sig = grad_sigma(p.amax) * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
+    const float sig = grad_scale(p.range, bk) * exp2f(-WinScale<T>::kP);
     const float2* rows = p.terms + (static_cast<long long>(bidx) * p.h + kvh * p.g + hl0) * p.nq;
     int tl = tl0;
     for (int t = 0; t < n_it; ++t) {
@@ -591,13 +639,13 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------- elementwise
-    grid_wait();  // max |dO|
+    grid_wait();  // dS's range
     const int e = warp & 3, cc = (warp - 4) >> 2;  // columns 32 cc ..
     const int kr = e * 32 + lane, key = kb + kr;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
     const float c = p.scale * kLog2e;
-    const float sigma = grad_sigma(p.amax);
-    const float sig = sigma * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
+    const float scale = grad_scale(p.range, bk);
+    const float sig = scale * exp2f(-WinScale<T>::kP);
     int tl = tl0;
     bool ok = n_it > 0;
     for (int t = 0; t < n_it && ok; ++t) {
@@ -653,7 +701,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     tc_fence_after();
     // even column groups store dV, odd ones dK, 64 columns each
     const int half = cc & 1, c0 = 64 * (cc >> 1);
-    const float f = half == 0 ? exp2f(-WinScale<T>::kP) : p.scale / (sigma * WinScale<T>::kDS);
+    const float f = half == 0 ? exp2f(-WinScale<T>::kP) : p.scale / scale;
     const uint32_t acc = t_lane + (half == 0 ? C::TM_DV : C::TM_DK);
     if (slot0 >= 0) {
       if (done) {  // (a part without items writes nothing and is not read)
@@ -932,8 +980,8 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     const int qr = e * 32 + lane, i = qb * 128 + qr, pos = p0 + qr;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(e * 32) << 16);
     const float c = p.scale * kLog2e;
-    const float sigma = grad_sigma(p.amax);
-    const float sig = sigma * WinScale<T>::kDS * exp2f(-WinScale<T>::kP);
+    const float scale = grad_scale(p.range, static_cast<long long>(bidx) * p.hkv + kvh);
+    const float sig = scale * exp2f(-WinScale<T>::kP);
     float2 tr = make_float2(-INFINITY, 0.f);
     if (i < p.nq) tr = __ldcg(p.terms + (static_cast<long long>(bidx) * p.h + head) * p.nq + i);
     const float2 a2 = make_float2(tr.x, tr.x), nd2 = make_float2(tr.y * sig, tr.y * sig);
@@ -982,7 +1030,7 @@ __global__ void __launch_bounds__(kWinBwdThreads<D>, kWinBwdBlocks<D>)
     }
     const bool done = ok && mbar_wait_warp(acc_done, 0, abort_flag, p.err, kSiteAttnSoftmax);
     tc_fence_after();
-    const float f = p.scale / (sigma * WinScale<T>::kDS);
+    const float f = p.scale / scale;
     // 32 columns per warp, staged where the keys were: every product is done
     static_assert(D / 32 == C::QT / 32, "a column group per warp");
     static_assert(kWinElemWarps<D> * 2048 <= C::QK_SLOTS * C::STREAM, "staging");

@@ -321,10 +321,9 @@ cudaError_t launch_window(const CUtensorMap& q, const CUtensorMap& k, const CUte
 struct WindowBwdPlan {
   int part_len;
   int64_t parts, cut_parts, cut_blocks;  // per (sequence, kv head)
-  size_t off_terms, off_part, total;
+  size_t off_terms, off_range, range_bytes, off_part, total;
 };
 constexpr int kPlanSms = 148;  // the GPU the work is cut for
-constexpr size_t kAmaxOffset = 64;
 
 WindowBwdPlan window_bwd_plan(const bpt_window* w) {
   WindowBwdPlan p{};
@@ -350,7 +349,9 @@ WindowBwdPlan window_bwd_plan(const bpt_window* w) {
     }
   }
   p.off_terms = kOpsHeader;
-  p.off_part = align_to(p.off_terms + size_t(w->batch * w->heads) * size_t(w->n_q) * 8, 256);
+  p.off_range = align_to(p.off_terms + size_t(w->batch * w->heads) * size_t(w->n_q) * 8, 256);
+  p.range_bytes = w->dtype == BPT_F16 ? size_t(w->batch * w->kv_heads) * 8 : 0;
+  p.off_part = align_to(p.off_range + p.range_bytes, 256);
   p.total = align_to(p.off_part + size_t(w->batch * w->kv_heads) * size_t(p.cut_parts) *
                                       size_t(2 * 128 * 4) * size_t(w->d_k), 256);
   return p;
@@ -385,13 +386,15 @@ cudaError_t launch_early(K kernel, dim3 grid, unsigned threads, size_t smem, cud
 
 template <typename T, int D>
 cudaError_t launch_window_bwd(const CUtensorMap* stay, const CUtensorMap* stream,
-                              const bpt::WindowTermsParams& tp,
-                              const bpt::WindowBwdParams& p, const WindowBwdPlan& plan,
-                              int64_t batch, cudaStream_t s) {
+                              bpt::WindowTermsParams tp, const bpt::WindowBwdParams& p,
+                              const WindowBwdPlan& plan, int64_t batch, cudaStream_t s) {
   using C = bpt::WindowBwdCfg<D>;
-  const int64_t rows = int64_t(p.nq) * p.h, per = 256 / (D / 8) * bpt::kTermRows;
+  constexpr int64_t per = bpt::kTermBlockRows<D>;
+  tp.row_blocks = uint32_t((int64_t(p.nq) * p.g + per - 1) / per);
+  const int64_t value_blocks = tp.range != nullptr ? (int64_t(p.nkv) + per - 1) / per : 0;
   bpt::window_terms_kernel<T, D>
-      <<<dim3(unsigned((rows + per - 1) / per), unsigned(batch)), 256, 0, s>>>(tp);
+      <<<dim3(tp.row_blocks + unsigned(value_blocks), unsigned(p.hkv), unsigned(batch)), 256, 0, s>>>(
+          tp);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // dK/dV start on their products while the last terms are written; dQ's blocks,
@@ -692,21 +695,23 @@ bpt_status window_backward(const bpt_window* w, const bpt_rows* q, const bpt_row
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint32_t* amax = nullptr;
+  uint32_t* range = nullptr;
   if (w->dtype == BPT_F16) {
-    amax = reinterpret_cast<uint32_t*>(ws + kAmaxOffset);
-    if (cudaMemsetAsync(amax, 0, 4, s) != cudaSuccess) return BPT_ERR_CUDA;
+    range = reinterpret_cast<uint32_t*>(ws + plan.off_range);
+    if (cudaMemsetAsync(range, 0, plan.range_bytes, s) != cudaSuccess) return BPT_ERR_CUDA;
   }
   bpt::WindowTermsParams tp{};
   tp.o = o->data;
   tp.o_b = o->stride_b; tp.o_n = o->stride_n; tp.o_h = o->stride_h;
   tp.d_o = d_o->data;
   tp.d_b = d_o->stride_b; tp.d_n = d_o->stride_n; tp.d_h = d_o->stride_h;
+  tp.v = v->data;
+  tp.v_b = v->stride_b; tp.v_n = v->stride_n; tp.v_h = v->stride_h;
   tp.stats = reinterpret_cast<const float2*>(stats);
   tp.terms = reinterpret_cast<float2*>(ws + plan.off_terms);
-  tp.amax = amax;
+  tp.range = range;
   tp.lens = lens;
-  tp.B = int(B); tp.nq = int(nq); tp.nkv = int(nkv); tp.h = int(h);
+  tp.nq = int(nq); tp.nkv = int(nkv); tp.h = int(h); tp.g = int(h / hkv);
   tp.err = err;
   bpt::WindowBwdParams p{};
   p.nq = int(nq); p.nkv = int(nkv); p.h = int(h); p.hkv = int(hkv); p.g = int(h / hkv);
@@ -715,7 +720,7 @@ bpt_status window_backward(const bpt_window* w, const bpt_rows* q, const bpt_row
   p.sinks = int(std::min<int64_t>(w->sinks, nkv));
   p.lens = lens;
   p.terms = tp.terms;
-  p.amax = amax;
+  p.range = reinterpret_cast<const uint2*>(range);
   p.dq = dq->data;
   p.dq_b = dq->stride_b; p.dq_n = dq->stride_n; p.dq_h = dq->stride_h;
   p.dk = dk->data;

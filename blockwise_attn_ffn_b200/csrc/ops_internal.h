@@ -9,9 +9,9 @@
 
 namespace bpt_host {
 
-// Head of every workspace of these operators: the error word, a word of the
-// windowed backward, the counters of the decode attention.  The same for all
-// sizes and operators, so that one workspace serves any of them in turn.
+// Head of every workspace of these operators: the error word and the counters
+// of the decode attention.  The same for all sizes and operators, so that one
+// workspace serves any of them in turn.
 constexpr size_t kOpsHeader = 4096;
 
 BPT_INTERNAL bpt_status cache_append(const bpt_cache* cache, const void* k_new, const void* v_new,

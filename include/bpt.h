@@ -762,7 +762,9 @@ bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const
  * no query sees), dk and dv summed over the query heads that share a kv head:
  *     P = exp(s - m) / l,  dS = P (d_o V^T - rowsum(d_o o)),
  *     dv = P^T d_o,  dk = dS^T q / sqrt(d_k),  dq = dS k / sqrt(d_k).
- * fp32 accumulation in a fixed order: results do not depend on timing.
+ * fp32 accumulation in a fixed order: results do not depend on timing.  fp16:
+ * dS is held scaled to the norms of d_o's and v's rows, per sequence and kv
+ * head, so it does not overflow where the gradients themselves fit.
  * Rows past a length are not read into any product (they may hold NaN); other
  * values have to be finite: one that is not may turn any gradient of its
  * sequence into NaN.  The three gradients may be the interleaved parts of one
