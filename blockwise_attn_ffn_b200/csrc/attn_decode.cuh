@@ -22,15 +22,17 @@
 //  - Each of the four warps takes 16 slots of a tile with its own ring of
 //    cp.async stages and its own softmax state: no block barrier until a
 //    (sequence, head) run ends.  The reference maximum moves only when it
-//    grows by more than 2^8.
+//    grows by more than 2^8 (2^4 in fp16).
 // A run that covers all tiles of its pair writes the output; otherwise its
 // unnormalised fp32 accumulator and (m, l) go to the workspace, and the run
 // that comes last (a counter per run that starts
 // such a pair, left at zero again) joins the parts in
 // run order: one launch, and results do not depend on timing.  A second kernel
-// adds the weights up where they are wanted.  P is rounded to the cache's type for the PV product (relative
-// error half a step, averaged over the keys); scores, statistics and sums are
-// fp32.
+// adds the weights up where they are wanted.  P is rounded to the cache's type
+// for the PV product, half a step per weight; scores, statistics and sums are
+// fp32.  fp16 has its smallest step at 2^-24, and many small weights may count
+// beside one large: there P and l are held 2^11 times as large and the reference
+// moves sooner, so that a weight is off by 2^-36 of the reference at most.
 #pragma once
 
 #include <type_traits>
@@ -66,7 +68,7 @@ struct DecodeParams {
   uint32_t window, sinks;    // window 0: every slot
   float scale_log2;
   float* part_o;   // [2 * ctas][16][D]
-  float2* part_ml; // [2 * ctas][16]
+  float2* part_ml; // [2 * ctas][16]: m, and l as P is scaled
   float2* seg_ml;  // [B * h_kv * chunks][16]: joined (m, l), where weights are wanted
   uint32_t* count; // [ctas]: parts that are done of the pair that run c starts and does not end
   uint32_t ctas;   // grid of the split kernel
@@ -74,6 +76,15 @@ struct DecodeParams {
   long long scores_ld;
   const float* acc;  // nullable [B][h_kv][cap]
   float* acc_out;
+};
+
+// P is exp2(s - m + kShift) with a reference m that moves when the maximum grows
+// by more than 2^kGrow: at most 2^15 in fp16 (65504 is its largest value).
+template <typename T>
+struct DecodeScale {
+  static constexpr float kShift = std::is_same<T, __half>::value ? 11.f : 0.f;
+  static constexpr float kGrow = std::is_same<T, __half>::value ? 4.f : 8.f;
+  static constexpr float kUnit = std::is_same<T, __half>::value ? 0x1p-11f : 1.f;  // 2^-kShift
 };
 
 // The visible slots of a sequence as a dense list: index u -> slot.
@@ -236,7 +247,8 @@ __device__ __noinline__ void decode_join(const DecodeParams& p, uint32_t lo, uin
       a.w += f * x.w;
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    if (p.scores != nullptr && col == 0) p.seg_ml[seg * 16 + row] = make_float2(M, L);
+    if (p.scores != nullptr && col == 0)
+      p.seg_ml[seg * 16 + row] = make_float2(M, L * DecodeScale<T>::kUnit);
     *reinterpret_cast<uint2*>(out + row * p.o_h + col) =
         make_uint2(pack2<T>(a.x * inv, a.y * inv), pack2<T>(a.z * inv, a.w * inv));
   }
@@ -466,7 +478,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
         mx[nt][j] = v;
-        grow |= v > m[nt][j] + 8.f;  // (-inf + 8 = -inf: the first visible slot counts)
+        // (from -inf any score grows, and -inf itself, NaN here, does not)
+        grow |= v - m[nt][j] > DecodeScale<T>::kGrow;
       }
     }
     if (__any_sync(0xffffffffu, grow)) {
@@ -488,9 +501,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
     uint32_t pb[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      // a head that has seen nothing keeps reference 0: exp2(-inf) = 0
-      const float f0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-      const float f1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+      // a head that has seen nothing keeps reference 0: exp2(-inf) = 0; rounded
+      // up, so that P stays within its range for scores of any size
+      const float f0 = m[nt][0] == -INFINITY ? 0.f : __fadd_ru(m[nt][0], -DecodeScale<T>::kShift);
+      const float f1 = m[nt][1] == -INFINITY ? 0.f : __fadd_ru(m[nt][1], -DecodeScale<T>::kShift);
       s[nt][0] = ex2_approx(s[nt][0] - f0);
       s[nt][1] = ex2_approx(s[nt][1] - f1);
       s[nt][2] = ex2_approx(s[nt][2] - f0);
@@ -581,7 +595,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeShape<D, NT>::CTAS))
           *reinterpret_cast<float4*>(p.part_o + (ps * 16LL + row) * D + col) = v;
           continue;
         }
-        if (p.scores != nullptr && col == 0) p.seg_ml[seg * 16 + row] = make_float2(M, L);
+        if (p.scores != nullptr && col == 0)
+          p.seg_ml[seg * 16 + row] = make_float2(M, L * DecodeScale<T>::kUnit);
         const float inv = L > 0.f ? 1.f / L : 0.f;
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + cc.b * p.o_b + (head0 + row) * p.o_h +
                                   col) =
