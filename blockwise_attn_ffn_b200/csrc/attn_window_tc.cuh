@@ -25,9 +25,12 @@
 // The schedule is that of the dense kernel: warp 0 loads (TMA), warp 1 issues
 // PV_A(j), S_A(j+1), PV_B(j), S_B(j+1) ..., four warps per tile run the
 // softmax; P stays in tensor memory over S.  The reference moves only when a
-// row's maximum grows by more than 2^8 (exp2 units).  P is rounded to the
-// operands' type for the product with V (half a step per weight, of both
-// signs); scores, statistics and O are fp32; l sums the unrounded weights.
+// row's maximum grows by more than 2^8 (exp2 units; 2^6 in fp16).  P is rounded
+// to the operands' type for the product with V, half a step per weight; scores,
+// statistics and O are fp32; l sums the unrounded weights.  fp16 has its smallest
+// step at 2^-24, and many small weights may count beside one large: there P and
+// l are held 2^9 times as large, so that a weight is off by 2^-34 of the
+// reference at most.
 //
 // Measured at 65536 tokens, 16 heads of 128, window 4096, 4 sinks: 1.97 ms in
 // bursts (1082 TFLOP/s of visible pairs), 2.27 ms under the power cap.  With two
@@ -182,6 +185,18 @@ __device__ __forceinline__ uint32_t window_bits(int p, int kb, int lo, int windo
   return bits_range(max(p - window + 1 - kb, low), top, w) |
          bits_range(low, min(sinks - kb, top), w);
 }
+
+// P is exp2((S - m) c + kShift) with a reference m that moves when the row's
+// maximum grows by more than 2^kGrow: at most 2^15 in fp16 (65504 is its
+// largest value).  A smaller kGrow leaves room for a larger kShift, but O is
+// scaled more often.  Measured in fp16 at 65536 tokens, 16 heads of 128, window
+// 4096, 4 sinks, growth / shift 4 / 11, 5 / 10, 6 / 9, 7 / 8, 8 / 7: 2519, 2452,
+// 2341, 2318, 2324 us under the power cap; 8 / 0: 2354.
+template <typename T>
+struct WindowScale {
+  static constexpr float kShift = std::is_same<T, __half>::value ? 9.f : 0.f;
+  static constexpr float kGrow = std::is_same<T, __half>::value ? 6.f : 8.f;
+};
 
 // The largest of three values, NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
@@ -509,7 +524,7 @@ __global__ void __launch_bounds__(384, 1)
       float m_new = m_run;
       bool need = false;
       if (mx > m_run) {
-        need = (m_run == -INFINITY) || ((mx - m_run) * c > 8.0f);
+        need = (m_run == -INFINITY) || ((mx - m_run) * c > WindowScale<T>::kGrow);
         if (need) m_new = mx;
       }
       const bool warp_need = __any_sync(0xffffffffu, need) && o_live;
@@ -526,8 +541,12 @@ __global__ void __launch_bounds__(384, 1)
           tmem_st_32x32b_x8(tO + cc * 8, v);
         }
       }
-      // a row that has seen no key yet keeps reference 0: exp2(-inf) = 0
-      const float ref = m_new == -INFINITY ? 0.f : -m_new * c;
+      // a row that has seen no key yet keeps reference 0: exp2(-inf) = 0; rounded
+      // down in fp16, so that P stays within its range for large scores
+      float ref = -m_new * c;
+      if constexpr (WindowScale<T>::kShift != 0.f)
+        ref = __fmaf_rd(-m_new, c, WindowScale<T>::kShift);
+      if (m_new == -INFINITY) ref = 0.f;
       const float2 cc2 = make_float2(c, c), mref2 = make_float2(ref, ref);
       float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(384, 1)
       if (p.stats != nullptr && in_q) {
         // in the units of s = q.k / sqrt(d_k): m the exact maximum, l relative to it
         const float m_s = m_true * c * 0.69314718055994531f;
-        const float l_s = l * ex2_approx((m_run - m_true) * c);
+        const float l_s = l * ex2_approx((m_run - m_true) * c - WindowScale<T>::kShift);
         p.stats[(static_cast<long long>(bidx) * p.h + head) * p.nq + i] =
             valid ? make_float2(m_s, l_s) : make_float2(-INFINITY, 0.f);
       }
