@@ -308,6 +308,59 @@ bool rows_apart(const bpt_rows& r, int64_t batch, int64_t n, int64_t heads, int6
   return true;
 }
 
+// Whether rows of a and b meet.  Rows at elements x and y share one if
+// |delta + sum of the indexes times their strides| < d_k, indexes of a counting
+// down and of b up; dimensions that both have with one stride count as one, from
+// 1 - n_a to n_b - 1.  From the largest stride down, only the indexes that the
+// smaller ones can make up for are followed: a handful for tensors whose own rows
+// are apart.  More than kMeetSteps count as a meeting.
+constexpr int kMeetSteps = 4096;
+struct MeetDim {
+  int64_t stride, lo, hi;
+};
+bool meet_from(const MeetDim* d, int n, int64_t at, int64_t dk, int* steps) {
+  if (++*steps > kMeetSteps) return true;
+  if (n == 0) return at > -dk && at < dk;
+  int64_t lo = at, hi = at;  // what the smaller dimensions can reach
+  for (int i = 1; i < n; ++i) {
+    lo += d[i].lo * d[i].stride;
+    hi += d[i].hi * d[i].stride;
+  }
+  // x stride + [lo, hi] meets (-dk, dk)
+  auto floor_div = [](int64_t a, int64_t b) { return a >= 0 ? a / b : -((-a + b - 1) / b); };
+  const int64_t first = std::max(d[0].lo, -floor_div(dk - 1 + hi, d[0].stride));
+  const int64_t last = std::min(d[0].hi, floor_div(dk - 1 - lo, d[0].stride));
+  for (int64_t x = first; x <= last; ++x)
+    if (meet_from(d + 1, n - 1, at + x * d[0].stride, dk, steps)) return true;
+  return false;
+}
+bool rows_meet(const bpt_rows& a, const int64_t (&na)[3], const bpt_rows& b, const int64_t (&nb)[3],
+               int64_t dk) {
+  const int64_t sa[3] = {a.stride_b, a.stride_n, a.stride_h};
+  const int64_t sb[3] = {b.stride_b, b.stride_n, b.stride_h};
+  if (!Range(a.data, extent({{na[0], sa[0]}, {na[1], sa[1]}, {na[2], sa[2]}}, dk))
+           .meets(Range(b.data, extent({{nb[0], sb[0]}, {nb[1], sb[1]}, {nb[2], sb[2]}}, dk))))
+    return false;
+  MeetDim d[6];
+  int n = 0;
+  for (int i = 0; i < 3; ++i)
+    if (na[i] > 1) d[n++] = {sa[i], 1 - na[i], 0};
+  for (int i = 0; i < 3; ++i) {
+    if (nb[i] <= 1) continue;
+    int k = 0;
+    while (k < n && !(d[k].stride == sb[i] && d[k].hi == 0)) ++k;
+    if (k < n)
+      d[k].hi = nb[i] - 1;
+    else
+      d[n++] = {sb[i], 0, nb[i] - 1};
+  }
+  std::sort(d, d + n, [](const MeetDim& x, const MeetDim& y) { return x.stride > y.stride; });
+  const auto pa = reinterpret_cast<uintptr_t>(a.data), pb = reinterpret_cast<uintptr_t>(b.data);
+  const int64_t delta = pb >= pa ? int64_t((pb - pa) / 2) : -int64_t((pa - pb) / 2);
+  int steps = 0;
+  return meet_from(d, n, delta, dk, &steps);
+}
+
 template <typename T, int D>
 cudaError_t launch_window(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                           const bpt::WindowParams& p, int64_t batch, cudaStream_t s) {
@@ -660,20 +713,23 @@ bpt_status window_backward(const bpt_window* w, const bpt_rows* q, const bpt_row
       !rows_apart(*dv, B, nkv, hkv, c) || stats == nullptr || unaligned(stats, 8) ||
       unaligned(lens, 4) || workspace == nullptr || unaligned(workspace, 256))
     return BPT_ERR_INVALID_ARG;
+  // Gradients may interleave with one another (the parts of one packed
+  // gradient), but share no row, and they meet nothing that is read (below).
+  const int64_t by_q[3] = {B, nq, h}, by_k[3] = {B, nkv, hkv};
+  if (rows_meet(*dq, by_q, *dk, by_k, c) || rows_meet(*dq, by_q, *dv, by_k, c) ||
+      rows_meet(*dk, by_k, *dv, by_k, c))
+    return BPT_ERR_INVALID_ARG;
   const WindowBwdPlan plan = window_bwd_plan(w);
   if (workspace_bytes < plan.total) return BPT_ERR_WORKSPACE;
   const Range rq = rows_range(*q, B, nq, h, c), rk = rows_range(*k, B, nkv, hkv, c),
               rv = rows_range(*v, B, nkv, hkv, c), ro = rows_range(*o, B, nq, h, c),
               rd = rows_range(*d_o, B, nq, h, c), rl(lens, size_t(B) * 4),
               rs(stats, size_t(B * h) * size_t(nq) * 8), rw(workspace, plan.total);
-  // Gradients may interleave with one another (the parts of one packed
-  // gradient), not with what is read.
   for (const Range& r : {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
                          rows_range(*dv, B, nkv, hkv, c), rw})
     if (any_meets(r, {rq, rk, rv, ro, rd, rl, rs})) return BPT_ERR_INVALID_ARG;
   if (any_meets(rw, {rows_range(*dq, B, nq, h, c), rows_range(*dk, B, nkv, hkv, c),
-                     rows_range(*dv, B, nkv, hkv, c)}) ||
-      dq->data == dk->data || dq->data == dv->data || dk->data == dv->data)
+                     rows_range(*dv, B, nkv, hkv, c)}))
     return BPT_ERR_INVALID_ARG;
   int sms = 0;
   st = ops_device(&sms);

@@ -768,7 +768,8 @@ bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const
  * Rows past a length are not read into any product (they may hold NaN); other
  * values have to be finite: one that is not may turn any gradient of its
  * sequence into NaN.  The three gradients may be the interleaved parts of one
- * packed tensor; they may not overlap what is read.  n_q = 0 with n_kv > 0 is
+ * packed tensor; they may share no element (BPT_ERR_INVALID_ARG) and may not
+ * overlap what is read.  n_q = 0 with n_kv > 0 is
  * refused; batch, heads and batch * kv_heads are at most 65535.
  */
 bpt_status bpt_attn_window_backward_workspace_size(const bpt_window* w, size_t* bytes);
