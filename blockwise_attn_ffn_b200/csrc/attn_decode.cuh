@@ -652,7 +652,8 @@ __global__ void __launch_bounds__(kWeightThreads) attn_decode_weights_kernel(con
     const uint32_t ck = r / p.rows, row = r - ck * p.rows;
     const long long seg = (static_cast<long long>(b) * p.c.hkv + kvh) * p.chunks + ck;
     const float2 v = p.seg_ml[seg * 16 + row];
-    ml_sh[r] = make_float2(v.x == -INFINITY ? 0.f : v.x, v.y > 0.f ? 1.f / v.y : 0.f);
+    // (l = 0: no slot was visible; l = NaN makes every weight NaN)
+    ml_sh[r] = make_float2(v.x == -INFINITY ? 0.f : v.x, v.y == 0.f ? 0.f : 1.f / v.y);
   }
   __syncthreads();
   const long long a0 = (static_cast<long long>(b) * p.c.hkv + kvh) * p.c.cap;

@@ -689,7 +689,8 @@ bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recen
  * (append the new token first, so that it sees itself).  A sequence without
  * visible slots gets zeros.  acc, acc_out (both or neither): for every slot
  * j < lens[b], acc_out = acc + the sum over the kv head's query heads of the
- * softmax weights (slots that are not visible add 0); acc_out may be acc.
+ * softmax weights (slots that are not visible add 0); acc_out may be acc.  A
+ * visible score of NaN or +inf makes the output and all weights of its head NaN.
  * Scores, softmax statistics and sums are fp32; results do not depend on
  * timing (no atomics).
  */
