@@ -723,6 +723,10 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
  * Only what a row sees counts: NaN and infinities in keys and values that it
  * does not see (masked ones, padding) do not reach its output.  A score of NaN
  * or +inf that it does see makes its output and its l NaN, as in a softmax.
+ * Values of V that are not finite cost time: the columns that hold them are done
+ * again, for every row that sees them or has them in a tile of its keys (near its
+ * window's ends, or among the first 128 keys with sinks), at up to 50 times a row's
+ * usual time; until they are all NaN where they are seen.
  *
  * Workspaces: as for the cache's operators.
  */
