@@ -302,6 +302,8 @@ def layer_forward_window(x: torch.Tensor, p: Dict[str, torch.Tensor], h: int, wi
     c = None
     slots = ()
     if cache is not None:
+        if cache[0].get_device() != index:
+            raise ValueError(f"the cache must be on cuda:{index} like x, got {cache[0].device}")
         c = cache_struct(*cache)
         slots = (B, c.kv_heads, c.max_pages * c.page_size)
     st = run(_lib.bpt_layer_forward_window, index, *ptrs, B, N, d, h, d_ff, code, window, sinks,
