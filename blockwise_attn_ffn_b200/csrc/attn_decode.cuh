@@ -122,8 +122,9 @@ __device__ __forceinline__ uint32_t run_of(uint32_t W, uint32_t G, uint32_t x) {
 // K and V rows are read once per call: in L2 they make room for one another
 // first, not for the scores, the parts to join or what else the program keeps
 // there.  Measured after writes that fill L2: 64 ragged sequences up to 8192
-// slots, 32 heads of 128 on 8, with weights 291 -> 274 us, without 249 -> 251;
-// 131072 slots of one sequence 123 -> 111.  Call after call: 266 -> 267, 335 -> 332.
+// slots, 32 heads of 128 on 8, with weights 291 -> 274 us; 131072 slots of one
+// sequence 123 -> 111.  Without weights (249, 251), and call after call (266, 267;
+// 335, 332), the difference is within noise.
 __device__ __forceinline__ uint64_t evict_first_policy() {
   uint64_t policy;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));

@@ -19,10 +19,10 @@
 //   window_join_kernel    adds the parts of blocks that were cut.
 // 7 products of 2 d_k flops per pair for the 5 of the formulas: S and dP are
 // computed twice, which keeps dQ out of memory and results independent of
-// timing.  Measured at 16384 tokens, 16 heads of 128 on 4, window 2048: 0.84 ms in
-// bursts; alone, dK/dV take 505 us (3000 clocks per 128 x 128 step for 2048 of
-// products: P, dV and the next scores, which go where P lies, follow one
-// another), dQ 409, terms 31.
+// timing.  Measured at 16384 tokens, 16 heads of 128 on 4, window 2048, fp16: 0.84
+// ms in bursts; one after the other and alone, dK/dV take 505 us (3000 clocks per
+// 128 x 128 step for 2048 of products: P, dV and the next scores, which go where P
+// lies, follow one another), dQ 379, terms 35, the join 7.
 //
 // The launches overlap (programmatic launches).  dK/dV blocks do all but the
 // row terms while the last terms are written.  dQ needs the terms, not dK/dV:

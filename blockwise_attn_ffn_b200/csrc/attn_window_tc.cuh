@@ -32,8 +32,8 @@
 // l are held 2^9 times as large, so that a weight is off by 2^-34 of the
 // reference at most.
 //
-// Measured at 65536 tokens, 16 heads of 128, window 4096, 4 sinks: 1.97 ms in
-// bursts (1082 TFLOP/s of visible pairs), 2.27 ms under the power cap.  With two
+// Measured at 65536 tokens, 16 heads of 128, window 4096, 4 sinks: 1.95 ms in
+// bursts (1093 TFLOP/s of visible pairs), 2.29 ms under the power cap.  With two
 // threads per row (maxima exchanged through shared memory) it took 2.18 to 2.35
 // ms: the exponentials of a tile keep the scheduler's unit busy as long, and the
 // exchange comes on top.

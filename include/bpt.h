@@ -673,6 +673,12 @@ bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const voi
  * written.  n <= budget: acc and pos are copied, no row moves.
  * new_lens[b] = min(n, budget).  acc_out may be acc, pos_out pos and new_lens
  * lens (exactly); they may not overlap otherwise.
+ * Slots are then no longer in the order of positions, and each head has tokens of
+ * its own in them: the window and sinks of bpt_attn_decode and bpt_layer_decode,
+ * which go by slot, mean nothing on an evicted cache (use window = 0 and this
+ * call's sinks and recent; positions of new tokens come from seen).  Tokens that
+ * were appended start with acc = 0, a prompt's too: an eviction before any step
+ * has added weights keeps the lowest slots.
  */
 bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recent, int64_t sinks,
                            const float* acc, const int32_t* pos, const int32_t* seen,
@@ -684,7 +690,8 @@ bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recen
  * q, out: [batch, heads, d_k] of the cache's type, element strides
  * (multiples of 8) given; kv_heads divides heads, head t reads kv head
  * t / (heads / kv_heads), at most 256 heads per kv head.  Slot j < lens[b] is
- * visible if window == 0, j >= lens[b] - window or j < sinks:
+ * visible if window == 0, j >= lens[b] - window or j < sinks (by slot: a window
+ * is for caches that were never evicted from):
  *   out[b, t] = sum_j softmax_j(q . k_j / sqrt(d_k)) v_j
  * (append the new token first, so that it sees itself).  A sequence without
  * visible slots gets zeros.  acc, acc_out (both or neither): for every slot
