@@ -132,17 +132,17 @@ bpt_status check_cache(const bpt_cache* c) {
     return BPT_ERR_UNSUPPORTED;
   return BPT_OK;
 }
+size_t cache_bytes(const bpt_cache* c) {
+  return size_t(c->pages) * size_t(c->kv_heads * c->page_size) * size_t(c->d_k) * 2;
+}
 bpt_status check_cache_pointers(const bpt_cache* c) {
   for (const void* p : {c->k, c->v})
     if (p == nullptr || unaligned(p, 16)) return BPT_ERR_INVALID_ARG;
   for (const int32_t* p : {c->page_table, c->lens})
     if (p == nullptr || unaligned(p, 4)) return BPT_ERR_INVALID_ARG;
-  const size_t n = size_t(c->pages) * size_t(c->kv_heads * c->page_size) * size_t(c->d_k) * 2;
+  const size_t n = cache_bytes(c);
   if (Range(c->k, n).meets(Range(c->v, n))) return BPT_ERR_INVALID_ARG;
   return BPT_OK;
-}
-size_t cache_bytes(const bpt_cache* c) {
-  return size_t(c->pages) * size_t(c->kv_heads * c->page_size) * size_t(c->d_k) * 2;
 }
 size_t slots_bytes(const bpt_cache* c) {  // [batch][kv_heads][max_pages * page_size] words
   return size_t(c->batch) * size_t(c->kv_heads) * size_t(c->max_pages * c->page_size) * 4;
@@ -469,10 +469,10 @@ cudaError_t launch_window_bwd(const CUtensorMap* stay, const CUtensorMap* stream
 namespace bpt_host {
 
 bpt_status cache_append(const bpt_cache* cache, const void* k_new, const void* v_new,
-                            int64_t tokens, const int64_t* strides, const int32_t* counts,
-                            int32_t* new_lens, float* acc, int32_t* pos, const int32_t* seen,
-                            void* workspace, size_t workspace_bytes, bpt_stream_t stream, uint32_t* err,
-                         bool check_only) {
+                        int64_t tokens, const int64_t* strides, const int32_t* counts,
+                        int32_t* new_lens, float* acc, int32_t* pos, const int32_t* seen,
+                        void* workspace, size_t workspace_bytes, bpt_stream_t stream,
+                        uint32_t* err, bool check_only) {
   if (err == nullptr) err = static_cast<uint32_t*>(workspace);
   bpt_status st = check_cache(cache);
   if (st != BPT_OK) return st;
@@ -538,11 +538,10 @@ bpt_status cache_append(const bpt_cache* cache, const void* k_new, const void* v
 }
 
 bpt_status attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
-                           int64_t q_stride_b, int64_t q_stride_h, int64_t window, int64_t sinks,
-                           const float* acc, float* acc_out, void* out, int64_t out_stride_b,
-                           int64_t out_stride_h, void* workspace, size_t workspace_bytes,
-                           bpt_stream_t stream, uint32_t* err,
-                         bool check_only) {
+                       int64_t q_stride_b, int64_t q_stride_h, int64_t window, int64_t sinks,
+                       const float* acc, float* acc_out, void* out, int64_t out_stride_b,
+                       int64_t out_stride_h, void* workspace, size_t workspace_bytes,
+                       bpt_stream_t stream, uint32_t* err, bool check_only) {
   if (err == nullptr) err = static_cast<uint32_t*>(workspace);
   bpt_status st = check_cache(cache);
   if (st != BPT_OK) return st;
@@ -626,9 +625,9 @@ bpt_status attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
 }
 
 bpt_status window_forward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
-                                   const bpt_rows* v, const int32_t* lens, const bpt_rows* out,
-                                   float* stats, void* workspace, size_t workspace_bytes,
-                                   bpt_stream_t stream, uint32_t* err) {
+                          const bpt_rows* v, const int32_t* lens, const bpt_rows* out,
+                          float* stats, void* workspace, size_t workspace_bytes,
+                          bpt_stream_t stream, uint32_t* err) {
   if (err == nullptr) err = static_cast<uint32_t*>(workspace);
   bpt_status st = check_window(w);
   if (st != BPT_OK) return st;
@@ -691,10 +690,10 @@ bpt_status window_forward(const bpt_window* w, const bpt_rows* q, const bpt_rows
 }
 
 bpt_status window_backward(const bpt_window* w, const bpt_rows* q, const bpt_rows* k,
-                                    const bpt_rows* v, const bpt_rows* o, const float* stats,
-                                    const bpt_rows* d_o, const int32_t* lens, const bpt_rows* dq,
-                                    const bpt_rows* dk, const bpt_rows* dv, void* workspace,
-                                    size_t workspace_bytes, bpt_stream_t stream, uint32_t* err) {
+                           const bpt_rows* v, const bpt_rows* o, const float* stats,
+                           const bpt_rows* d_o, const int32_t* lens, const bpt_rows* dq,
+                           const bpt_rows* dk, const bpt_rows* dv, void* workspace,
+                           size_t workspace_bytes, bpt_stream_t stream, uint32_t* err) {
   if (err == nullptr) err = static_cast<uint32_t*>(workspace);
   bpt_status st = check_window_bwd(w);
   if (st != BPT_OK) return st;
@@ -815,7 +814,8 @@ bpt_status bpt_cache_append(const bpt_cache* cache, const void* k_new, const voi
                             int64_t tokens, const int64_t* strides, const int32_t* counts,
                             int32_t* new_lens, float* acc, int32_t* pos, const int32_t* seen,
                             void* workspace, size_t workspace_bytes, bpt_stream_t stream) {
-  return bpt_host::cache_append(cache, k_new, v_new, tokens, strides, counts, new_lens, acc, pos, seen, workspace, workspace_bytes, stream, nullptr);
+  return bpt_host::cache_append(cache, k_new, v_new, tokens, strides, counts, new_lens, acc, pos,
+                                seen, workspace, workspace_bytes, stream, nullptr);
 }
 
 bpt_status bpt_cache_evict(const bpt_cache* cache, int64_t budget, int64_t recent, int64_t sinks,
@@ -926,7 +926,9 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
                            const float* acc, float* acc_out, void* out, int64_t out_stride_b,
                            int64_t out_stride_h, void* workspace, size_t workspace_bytes,
                            bpt_stream_t stream) {
-  return bpt_host::attn_decode(cache, q, heads, q_stride_b, q_stride_h, window, sinks, acc, acc_out, out, out_stride_b, out_stride_h, workspace, workspace_bytes, stream, nullptr);
+  return bpt_host::attn_decode(cache, q, heads, q_stride_b, q_stride_h, window, sinks, acc,
+                               acc_out, out, out_stride_b, out_stride_h, workspace,
+                               workspace_bytes, stream, nullptr);
 }
 
 bpt_status bpt_attn_window_workspace_size(const bpt_window* w, size_t* bytes) {
@@ -941,7 +943,8 @@ bpt_status bpt_attn_window_forward(const bpt_window* w, const bpt_rows* q, const
                                    const bpt_rows* v, const int32_t* lens, const bpt_rows* out,
                                    float* stats, void* workspace, size_t workspace_bytes,
                                    bpt_stream_t stream) {
-  return bpt_host::window_forward(w, q, k, v, lens, out, stats, workspace, workspace_bytes, stream, nullptr);
+  return bpt_host::window_forward(w, q, k, v, lens, out, stats, workspace, workspace_bytes, stream,
+                                  nullptr);
 }
 
 bpt_status bpt_attn_window_backward_workspace_size(const bpt_window* w, size_t* bytes) {
@@ -957,7 +960,8 @@ bpt_status bpt_attn_window_backward(const bpt_window* w, const bpt_rows* q, cons
                                     const bpt_rows* d_o, const int32_t* lens, const bpt_rows* dq,
                                     const bpt_rows* dk, const bpt_rows* dv, void* workspace,
                                     size_t workspace_bytes, bpt_stream_t stream) {
-  return bpt_host::window_backward(w, q, k, v, o, stats, d_o, lens, dq, dk, dv, workspace, workspace_bytes, stream, nullptr);
+  return bpt_host::window_backward(w, q, k, v, o, stats, d_o, lens, dq, dk, dv, workspace,
+                                   workspace_bytes, stream, nullptr);
 }
 
 }  // extern "C"
