@@ -732,8 +732,8 @@ bpt_status bpt_attn_decode(const bpt_cache* cache, const void* q, int64_t heads,
  * or +inf that it does see makes its output and its l NaN, as in a softmax.
  * Values of V that are not finite cost time: the columns that hold them are done
  * again, for every row that sees them or has them in a tile of its keys (near its
- * window's ends, or among the first 128 keys with sinks), at up to 50 times a row's
- * usual time; until they are all NaN where they are seen.
+ * window's ends, or among the first 128 keys with sinks), which takes about 100
+ * times a row's usual time, unless all of them are NaN from an early key on.
  *
  * Workspaces: as for the cache's operators.
  */

@@ -70,8 +70,8 @@ def test_whole_rows_of_bad_values():
 def test_one_bad_value_leaves_the_call_short(key, value):
     """A NaN in a sink that every row sees, an infinity that shares its tile:
     all 16384 rows of a head are done again.  Key by key that is 4100 dependent
-    steps of about 500 clocks for each of a warp's 32 rows, 35 ms; with the
-    keys in parallel about a tenth."""
+    steps for each of a warp's 32 rows, 71 ms in all; with the keys in parallel
+    about a tenth."""
     n, h, window = 16384, 8, 4096
     q, k, v = inputs(33, 1, n, n, h, h, 64, torch.bfloat16)
     out, ws = torch.empty_like(q), bpt.attn_window_workspace(q, k, window, 4)
